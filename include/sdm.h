@@ -88,7 +88,9 @@ typedef enum sdm_status {
  * rows), which applies the write to each decoded 16-value block in fp32 and
  * re-quantises it exactly as the decode step does. Other variants and the
  * backward return SDM_ERR_UNSUPPORTED for it. */
-typedef enum sdm_dtype { SDM_F32 = 0, SDM_BF16 = 1, SDM_FP8_B16 = 2 } sdm_dtype_t;
+/* SDM_FP8_ROW is an output dtype of sdm_rmsnorm_residual only: E4M3 codes with
+ * one fp32 scale per row (value = E4M3(code) * scale). */
+typedef enum sdm_dtype { SDM_F32 = 0, SDM_BF16 = 1, SDM_FP8_B16 = 2, SDM_FP8_ROW = 3 } sdm_dtype_t;
 
 /* Which recurrence kernel runs (sdm_shape_t.variant). */
 typedef enum sdm_variant {
@@ -464,6 +466,155 @@ SDM_API sdm_status_t sdm_layer_forward_noalloc(const sdm_shape_t* shape, const v
                                        const void* v, const void* alpha, const void* beta,
                                        const void* g, const void* M0, void* M_out, float* y,
                                        void* stream);
+
+/* ---- around the recurrent core: norm, convolution, selective scan, clipping ---- */
+
+/* RMS norm with the residual's addition: for each of n_rows rows of d values
+ *   h = round(x + residual) to res_dtype (h = x without a residual),
+ *   y = h / sqrt(mean(h^2) + eps) * w,
+ * with y rounded once to y_dtype: SDM_F32, SDM_BF16, or 8 bits with scales
+ * (d a multiple of 16), decided on the real y as if it were held exactly:
+ *   SDM_FP8_B16: y [n_rows * d] codes and scales [n_rows * d / 16] int8, what
+ *     sdm_quantize_fp8blk makes of the real y;
+ *   SDM_FP8_ROW: y [n_rows * d] codes and scales [n_rows] fp32, scale =
+ *     max|y| / 448 of the row rounded to fp32 (1 for a row of zeros, at least
+ *     2^-126), code = round-to-nearest-even of y / scale onto the E4M3 grid.
+ * Values that are not numbers give the code 0x7F and do not count for a scale.
+ *   x [n_rows, d] x_dtype; residual [n_rows, d] res_dtype or NULL; w [d] w_dtype
+ *   h [n_rows, d] res_dtype out, with a residual only; may be residual itself
+ *   y may be x itself where the types agree. d in [1, 8192]; rows that are a
+ *   multiple of 8 values are moved in 16-byte units. scales: as above, NULL
+ *   for the other types. */
+SDM_API sdm_status_t sdm_rmsnorm_residual(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype,
+                                  const void* w, int32_t w_dtype, int64_t n_rows, int32_t d, float eps, void* h,
+                                  void* y, int32_t y_dtype, void* scales, void* stream);
+
+/* fp32 or bf16 values of the 8-bit formats: out = E4M3(code) * 2^exps (per 16
+ * values; codes, exps as sdm_quantize_fp8blk writes them), or E4M3(code) *
+ * scales[row], rounded once to out_dtype. */
+SDM_API sdm_status_t sdm_dequantize_fp8blk(const uint8_t* codes, const int8_t* exps, int64_t n_blocks, void* out,
+                                   int32_t out_dtype, void* stream);
+SDM_API sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, int64_t n_rows, int32_t d,
+                                   void* out, int32_t out_dtype, void* stream);
+
+/* Bytes of workspace sdm_rmsnorm_residual_backward needs (0 for invalid sizes). */
+SDM_API size_t sdm_rmsnorm_residual_backward_workspace_bytes(int64_t n_rows, int32_t d);
+
+/* Gradient of sdm_rmsnorm_residual for dy = dL/dy and dh = dL/dh (NULL: none),
+ * with s = 1 / sqrt(mean(h^2) + eps) and G = w dy:
+ *   dx = dh + s G - h s^3 mean(G h)   (the derivative of x and of the residual)
+ *   dw = sum over rows of dy h s
+ * For an 8-bit output this is the derivative with the rounding passed over.
+ *   h [n_rows, d] h_dtype (x without a residual); w [d]; dy [n_rows, d] dy_dtype;
+ *   dh, dx [n_rows, d] h_dtype (dx may be dh, or dy where the types agree);
+ *   dw [d] fp32 out. Deterministic. */
+SDM_API sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtype, const void* w, int32_t w_dtype,
+                                           const void* dy, int32_t dy_dtype, const void* dh, int64_t n_rows,
+                                           int32_t d, float eps, void* dx, float* dw, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Short causal depthwise convolution over the tokens, with optional SiLU:
+ *   u_t = bias + sum_k w[:, k] x_{t-K+1+k},  y_t = u_t sigmoid(u_t) (silu != 0) or u_t.
+ *   x      [B,T,D] in_dtype with x_stride elements from token to token (0: D;
+ *          T * x_stride from row to row of the batch), aligned to its element
+ *   w      [D,K], bias [D] or NULL: w_dtype;  K in [2, 8]
+ *   state  [B,K-1,D] in_dtype or NULL: the K - 1 inputs before the first token
+ *          (zeros without one), oldest first; replaced by the last K - 1 inputs,
+ *          so consecutive calls continue one sequence (T = 1 to decode)
+ *   lengths [B] int32 or NULL: tokens of each row; y of later tokens is left as
+ *          it was and their x is not read. Values outside [0, T] are clamped
+ *          and set the device error word.
+ *   y      [B,T,D] in_dtype; must not overlap x. */
+SDM_API sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, const void* w, const void* bias,
+                            int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K, int32_t silu, void* state,
+                            const int32_t* lengths, void* y, void* stream);
+
+/* Bytes of workspace sdm_short_conv_backward needs (0 for invalid sizes). */
+SDM_API size_t sdm_short_conv_backward_workspace_bytes(int32_t B, int32_t T, int32_t D, int32_t K);
+
+/* Gradient of sdm_short_conv for dy = dL/dy and dstate = dL/d(final state)
+ * (NULL: none); state0 is the state that the forward started from (NULL: zeros).
+ *   dx [B,T,D] in_dtype (0 for tokens past a row's length); dw [D,K] fp32;
+ *   dbias [D] fp32 or NULL; dstate0 [B,K-1,D] in_dtype or NULL. Deterministic. */
+SDM_API sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in_dtype, const void* w,
+                                     const void* bias, int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K,
+                                     int32_t silu, const void* state0, const int32_t* lengths, const void* dy,
+                                     const void* dstate, void* dx, float* dw, float* dbias, void* dstate0,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sizes of a selective scan: B batch rows, T tokens, D channels, N in [1, 64]
+ * states a channel, G groups of D / G channels that share B and C. Strides are
+ * elements from token to token (0: contiguous; T * stride from row to row of
+ * the batch), so inputs may be slices of a wider projection. */
+typedef struct sdm_selscan_shape {
+  int32_t B, T, D, N, G;
+  int32_t in_dtype;  /* of x, dt, B, C, z, y */
+  int32_t softplus;  /* != 0: delta = softplus(dt + dt_bias); else delta = dt + dt_bias */
+  int32_t reserved;  /* 0 */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+} sdm_selscan_shape_t;
+
+/* Bytes of workspace sdm_selective_scan needs (0 where it needs none, and for
+ * invalid shapes). */
+SDM_API size_t sdm_selective_scan_workspace_bytes(const sdm_selscan_shape_t* shape);
+
+/* Selective state space scan: per channel d of group g, for each token
+ *   delta = softplus(dt + dt_bias),
+ *   h[n] <- exp(delta A[d,n]) h[n] + delta x B[g,n],
+ *   y = (sum_n C[g,n] h[n] + Dskip x) * z sigmoid(z).
+ *   x, dt, z [B,T,D], Bm, Cm [B,T,G,N] in_dtype, aligned to their element; z
+ *     may be NULL (no gate)
+ *   A [D,N], Dskip [D] or NULL, dt_bias [D] or NULL: fp32. A is finite and, for
+ *     a state that decays, negative.
+ *   lengths [B] int32 or NULL, as in sdm_short_conv
+ *   h0 [B,D,N] fp32 or NULL (zeros): the state before the first token;
+ *   hT [B,D,N] fp32 or NULL: the state after each row's last token; may be h0,
+ *     so that consecutive calls continue one sequence (T = 1 to decode)
+ *   y [B,T,D] in_dtype; must not overlap the inputs. */
+SDM_API sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x, const void* dt, const float* A,
+                                const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                const float* dt_bias, const int32_t* lengths, const float* h0, float* hT, void* y,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace sdm_selective_scan_backward needs (0 for invalid shapes). */
+SDM_API size_t sdm_selective_scan_backward_workspace_bytes(const sdm_selscan_shape_t* shape);
+
+/* Gradient of sdm_selective_scan for dy = dL/dy and dhT = dL/dhT (NULL: none).
+ * The states are computed again from h0 (checkpoints every 64 tokens in the
+ * workspace).
+ *   dx, ddt, dz (with z) [B,T,D], dB, dC [B,T,G,N]: in_dtype, contiguous, 0 for
+ *   tokens past a row's length; dA [D,N], dD [D], ddt_bias [D] fp32 (the last
+ *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL.
+ * Deterministic. */
+SDM_API sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const void* x, const void* dt,
+                                         const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                                         const void* z, const float* dt_bias, const int32_t* lengths,
+                                         const float* h0, const void* dy, const float* dhT, void* dx, void* ddt,
+                                         float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                                         float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of sdm_grad_norm_clip: n values at grad, scaled into out (NULL:
+ * counted in the norm only; grad itself: in place), SDM_F32 or SDM_BF16 each,
+ * aligned to their elements (16-byte aligned ones move in 16-byte units). */
+typedef struct sdm_grad_tensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype, out_dtype;
+} sdm_grad_tensor_t;
+
+/* Bytes of workspace sdm_grad_norm_clip needs for n_tensors tensors. */
+SDM_API size_t sdm_grad_norm_clip_workspace_bytes(int32_t n_tensors);
+
+/* Global 2-norm of all tensors' values together and the clipping by it:
+ *   norm = sqrt(sum_i sum grad_i^2),  c = min(1, max_norm / (norm + eps)),  out_i = c grad_i.
+ * tensors is a HOST array, read during the call. norm: one fp32 on the device.
+ * max_norm may be infinite (out_i = grad_i). Squares beyond fp32's range are
+ * summed in 64 bits; a norm that is not finite gives c = 0 or not a number, as
+ * the formula does. Outputs must not overlap other tensors. The sums have a
+ * fixed order. */
+SDM_API sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tensors, float max_norm, float eps,
+                                float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Waits for `stream`, then reads and clears the current device's error word
  * (shared by all streams of the device; see the conventions above).

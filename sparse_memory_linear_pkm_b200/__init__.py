@@ -18,12 +18,16 @@ import ctypes
 import torch
 
 from . import native, synth
+from .block import (dequantize_fp8blk, dequantize_fp8row, grad_norm_clip, rmsnorm_residual, rmsnorm_residual_backward,
+                    selective_scan, selective_scan_backward, short_conv, short_conv_backward)
 from .native import SdmError
 
 __all__ = ["pkm_topk", "scan", "state_init", "layer_forward", "layer_step", "slot_counts", "scan_describe",
            "scan_backward", "pkm_topk_backward", "rmsnorm_gate", "rmsnorm_gate_backward", "layer_backward",
            "quantize_fp8blk", "fp8blk_parts", "stream_check", "make_shape", "layer_checkpoint_size", "layer_forward_ckpt",
-           "scan_workspace_bytes", "layer_forward_workspace_bytes", "scan_variant", "SdmError", "synth", "native"]
+           "scan_workspace_bytes", "layer_forward_workspace_bytes", "scan_variant", "SdmError", "synth", "native",
+           "rmsnorm_residual", "rmsnorm_residual_backward", "dequantize_fp8blk", "dequantize_fp8row", "short_conv",
+           "short_conv_backward", "selective_scan", "selective_scan_backward", "grad_norm_clip"]
 
 _DTYPE = {torch.float32: native.F32, torch.bfloat16: native.BF16,
           torch.uint8: native.FP8_B16}  # a uint8 state buffer holds the block-scaled fp8 state

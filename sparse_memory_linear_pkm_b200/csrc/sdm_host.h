@@ -10,6 +10,7 @@
 #include <string>
 
 #include "sdm.h"
+#include "sdm_check.h"
 #include "pkm_topk.cuh"
 #include "pkm_topk_fast.cuh"
 #include "sdm_misc.cuh"
@@ -23,22 +24,6 @@ namespace sdm_host {
 
 using sdm::bf16;
 
-// Per-device facts and the device address of the error word.
-struct DeviceInfo {
-  int sms = 0;
-  int max_smem_optin = 0;
-  int smem_per_sm = 0;
-  unsigned* err = nullptr;
-  bool ready = false;
-};
-
-// Records msg as the calling thread's last error and returns s.
-sdm_status_t fail(sdm_status_t s, const std::string& msg);
-// SDM_ERR_CUDA (with the launch error named after `what`) if the last launch failed.
-sdm_status_t launch_status(const char* what);
-// Raises a kernel's dynamic shared-memory limit to at least smem on the current device.
-void set_smem(const void* kern, size_t smem);
-size_t in_size(int32_t dtype);
 size_t state_size(int32_t dtype);  // bytes of one state value (fp8 state: the code byte)
 int64_t slots_of(int32_t sqrt_n);
 

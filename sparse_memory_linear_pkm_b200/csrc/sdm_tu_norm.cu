@@ -1,0 +1,229 @@
+// Entry points and launches of the RMS norm with the residual's addition, its
+// 8-bit outputs and its gradient.
+
+#include <algorithm>
+
+#include "sdm_check.h"
+#include "sdm_norm.cuh"
+
+namespace sdm_host {
+
+using sdm::bf16;
+
+namespace {
+
+// Threads per row and block size. A row of up to 512 values takes a power-of-two
+// part of a warp (several rows a block, no block barrier); a longer one a block.
+struct NormPlan {
+  bool block, vec;
+  int tpr, threads, rpb;
+};
+NormPlan norm_plan(int32_t d) {
+  NormPlan p;
+  const int need = (d + 8 * sdm::kNormV - 1) / (8 * sdm::kNormV);
+  p.vec = d % 8 == 0;
+  p.block = need > 32;
+  if (p.block) {
+    p.tpr = (need + 31) / 32 * 32;
+    p.threads = p.tpr;
+    p.rpb = 1;
+  } else {
+    p.tpr = 1;
+    while (p.tpr < need) p.tpr *= 2;
+    if (d % 16 == 0 && p.tpr < 2) p.tpr = 2;  // an 8-bit block is two threads' halves
+    p.threads = 128;
+    p.rpb = p.threads / p.tpr;
+  }
+  return p;
+}
+
+// Blocks of a launch: as many as the rows need, at most what `per_sm` threads
+// on every SM hold (the blocks then loop over the rows).
+unsigned norm_grid(const NormPlan& p, int64_t n_rows, int sms, int per_sm) {
+  const int64_t need = (n_rows + p.rpb - 1) / p.rpb;
+  return static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(sms) * std::max(1, per_sm / p.threads)));
+}
+
+constexpr int kGradThreadsPerSm = 1024;
+
+sdm_status_t check_norm(int64_t n_rows, int32_t d, float eps) {
+  if (n_rows < 0) return fail(SDM_ERR_INVALID_ARGUMENT, "n_rows must be >= 0");
+  if (d < 1) return fail(SDM_ERR_INVALID_ARGUMENT, "d must be >= 1");
+  if (d > sdm::kNormMaxD)
+    return fail(SDM_ERR_UNSUPPORTED, "d above " + std::to_string(sdm::kNormMaxD));
+  if (!(eps >= 0.0f) || eps > 1e30f) return fail(SDM_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  return SDM_OK;
+}
+
+template <typename Tx, typename Tr, int kOut>
+void launch_norm(const NormPlan& p, unsigned grid, const sdm::NormArgs& a, cudaStream_t st) {
+  if (p.vec) {
+    if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, true><<<grid, p.threads, 0, st>>>(a);
+    else sdm::k_rmsnorm_residual<Tx, Tr, kOut, false, true><<<grid, p.threads, 0, st>>>(a);
+  } else if constexpr (kOut < sdm::kNormFp8Blk) {
+    if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, false><<<grid, p.threads, 0, st>>>(a);
+    else sdm::k_rmsnorm_residual<Tx, Tr, kOut, false, false><<<grid, p.threads, 0, st>>>(a);
+  }
+}
+
+template <typename Tx, typename Tr>
+void launch_norm_out(int out, const NormPlan& p, unsigned grid, const sdm::NormArgs& a, cudaStream_t st) {
+  switch (out) {
+    case sdm::kNormF32: launch_norm<Tx, Tr, sdm::kNormF32>(p, grid, a, st); break;
+    case sdm::kNormBf16: launch_norm<Tx, Tr, sdm::kNormBf16>(p, grid, a, st); break;
+    case sdm::kNormFp8Blk: launch_norm<Tx, Tr, sdm::kNormFp8Blk>(p, grid, a, st); break;
+    default: launch_norm<Tx, Tr, sdm::kNormFp8Row>(p, grid, a, st); break;
+  }
+}
+
+template <typename T, typename Tdy>
+void launch_norm_grad(const NormPlan& p, unsigned grid, const sdm::NormGradArgs& a, cudaStream_t st) {
+  if (p.vec) {
+    if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, true><<<grid, p.threads, 0, st>>>(a);
+    else sdm::k_rmsnorm_residual_backward<T, Tdy, false, true><<<grid, p.threads, 0, st>>>(a);
+  } else {
+    if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, false><<<grid, p.threads, 0, st>>>(a);
+    else sdm::k_rmsnorm_residual_backward<T, Tdy, false, false><<<grid, p.threads, 0, st>>>(a);
+  }
+}
+
+}  // namespace
+
+}  // namespace sdm_host
+
+using namespace sdm_host;
+
+extern "C" {
+
+sdm_status_t sdm_rmsnorm_residual(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype,
+                                  const void* w, int32_t w_dtype, int64_t n_rows, int32_t d, float eps, void* h,
+                                  void* y, int32_t y_dtype, void* scales, void* stream) {
+  sdm_status_t r;
+  if ((r = check_norm(n_rows, d, eps)) || (r = check_dtype(x_dtype, "x_dtype")) ||
+      (r = check_dtype(w_dtype, "w_dtype")))
+    return r;
+  const bool any = n_rows > 0, res = residual != nullptr;
+  if (res && (r = check_dtype(res_dtype, "res_dtype"))) return r;
+  if (y_dtype < SDM_F32 || y_dtype > SDM_FP8_ROW)
+    return fail(SDM_ERR_INVALID_ARGUMENT, "y_dtype is not SDM_F32, SDM_BF16, SDM_FP8_B16 or SDM_FP8_ROW");
+  const bool fp8 = y_dtype >= SDM_FP8_B16;
+  if (fp8 && d % 16 != 0) return fail(SDM_ERR_INVALID_ARGUMENT, "an 8-bit output needs d a multiple of 16");
+  if ((r = need_ptr(x, "x", any)) || (r = need_ptr(w, "w", any)) || (r = need_ptr(residual, "residual", any && res)) ||
+      (r = need_ptr(h, "h", any && res)) || (r = need_ptr(y, "y", any)))
+    return r;
+  if (any && fp8 && scales == nullptr) return fail(SDM_ERR_INVALID_ARGUMENT, "scales is NULL");
+  if (any && y_dtype == SDM_FP8_ROW && reinterpret_cast<uintptr_t>(scales) % 4 != 0)
+    return fail(SDM_ERR_INVALID_ARGUMENT, "scales is not aligned to its element size");
+  if (!any) return ok();
+  DeviceInfo* dev;
+  if ((r = device_info(&dev)) != SDM_OK) return r;
+  const NormPlan p = norm_plan(d);
+  const sdm::NormArgs a{x, residual, w, h, y, scales, n_rows, d, p.tpr, w_dtype == SDM_BF16, eps};
+  const unsigned grid = norm_grid(p, n_rows, dev->sms, 4096);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool rb = res ? res_dtype == SDM_BF16 : true;
+  if (x_dtype == SDM_BF16) {
+    if (rb) launch_norm_out<bf16, bf16>(y_dtype, p, grid, a, st);
+    else launch_norm_out<bf16, float>(y_dtype, p, grid, a, st);
+  } else {
+    if (rb) launch_norm_out<float, bf16>(y_dtype, p, grid, a, st);
+    else launch_norm_out<float, float>(y_dtype, p, grid, a, st);
+  }
+  if ((r = launch_status("rmsnorm_residual launch")) != SDM_OK) return r;
+  return ok();
+}
+
+sdm_status_t sdm_dequantize_fp8blk(const uint8_t* codes, const int8_t* exps, int64_t n_blocks, void* out,
+                                   int32_t out_dtype, void* stream) {
+  sdm_status_t r;
+  if (n_blocks < 0) return fail(SDM_ERR_INVALID_ARGUMENT, "n_blocks must be >= 0");
+  if ((r = check_dtype(out_dtype, "out_dtype")) != SDM_OK) return r;
+  const bool any = n_blocks > 0;
+  if ((r = need_ptr(codes, "codes", any)) || (r = need_ptr(out, "out", any))) return r;
+  if (any && exps == nullptr) return fail(SDM_ERR_INVALID_ARGUMENT, "exps is NULL");
+  if (!any) return ok();
+  DeviceInfo* dev;
+  if ((r = device_info(&dev)) != SDM_OK) return r;
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>((n_blocks + 255) / 256, static_cast<int64_t>(dev->sms) * 32));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (out_dtype == SDM_BF16)
+    sdm::k_dequantize_fp8blk<bf16><<<grid, 256, 0, st>>>(codes, exps, n_blocks, static_cast<bf16*>(out));
+  else sdm::k_dequantize_fp8blk<float><<<grid, 256, 0, st>>>(codes, exps, n_blocks, static_cast<float*>(out));
+  if ((r = launch_status("dequantize_fp8blk launch")) != SDM_OK) return r;
+  return ok();
+}
+
+sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, int64_t n_rows, int32_t d, void* out,
+                                   int32_t out_dtype, void* stream) {
+  sdm_status_t r;
+  if (n_rows < 0) return fail(SDM_ERR_INVALID_ARGUMENT, "n_rows must be >= 0");
+  if (d < 16 || d % 16 != 0) return fail(SDM_ERR_INVALID_ARGUMENT, "d must be a multiple of 16");
+  if ((r = check_dtype(out_dtype, "out_dtype")) != SDM_OK) return r;
+  const bool any = n_rows > 0;
+  if ((r = need_ptr(codes, "codes", any)) || (r = need_gate(scales, "scales", any, SDM_F32)) ||
+      (r = need_ptr(out, "out", any)))
+    return r;
+  if (!any) return ok();
+  DeviceInfo* dev;
+  if ((r = device_info(&dev)) != SDM_OK) return r;
+  const int64_t units = n_rows * (d / 16);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>((units + 255) / 256, static_cast<int64_t>(dev->sms) * 32));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (out_dtype == SDM_BF16)
+    sdm::k_dequantize_fp8row<bf16><<<grid, 256, 0, st>>>(codes, scales, units, d / 16, static_cast<bf16*>(out));
+  else sdm::k_dequantize_fp8row<float><<<grid, 256, 0, st>>>(codes, scales, units, d / 16, static_cast<float*>(out));
+  if ((r = launch_status("dequantize_fp8row launch")) != SDM_OK) return r;
+  return ok();
+}
+
+size_t sdm_rmsnorm_residual_backward_workspace_bytes(int64_t n_rows, int32_t d) {
+  if (check_norm(n_rows, d, 0.0f) != SDM_OK) return 0;
+  ok();
+  if (n_rows == 0) return 0;
+  // One slot of d sums per row group of the largest grid of any device (a
+  // B200 has 148 SMs; the launch keeps to this many).
+  const NormPlan p = norm_plan(d);
+  return align256(static_cast<size_t>(norm_grid(p, n_rows, 148, kGradThreadsPerSm)) * p.rpb * d * sizeof(float));
+}
+
+sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtype, const void* w, int32_t w_dtype,
+                                           const void* dy, int32_t dy_dtype, const void* dh, int64_t n_rows,
+                                           int32_t d, float eps, void* dx, float* dw, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  sdm_status_t r;
+  if ((r = check_norm(n_rows, d, eps)) || (r = check_dtype(h_dtype, "h_dtype")) ||
+      (r = check_dtype(w_dtype, "w_dtype")) || (r = check_dtype(dy_dtype, "dy_dtype")))
+    return r;
+  const bool any = n_rows > 0;
+  if ((r = need_ptr(dw, "dw", true)) || (r = need_ptr(h, "h", any)) || (r = need_ptr(w, "w", any)) ||
+      (r = need_ptr(dy, "dy", any)) || (r = need_ptr(dh, "dh", any && dh != nullptr)) || (r = need_ptr(dx, "dx", any)))
+    return r;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!any) {
+    if (cudaMemsetAsync(dw, 0, static_cast<size_t>(d) * sizeof(float), st) != cudaSuccess)
+      return launch_status("dw clear");
+    return ok();
+  }
+  if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
+  if (workspace_bytes < sdm_rmsnorm_residual_backward_workspace_bytes(n_rows, d))
+    return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_rmsnorm_residual_backward_workspace_bytes");
+  const NormPlan p = norm_plan(d);
+  const unsigned grid = norm_grid(p, n_rows, 148, kGradThreadsPerSm);
+  float* part = static_cast<float*>(workspace);
+  const sdm::NormGradArgs a{h, w, dy, dh, dx, part, n_rows, d, p.tpr, w_dtype == SDM_BF16, eps};
+  if (h_dtype == SDM_BF16) {
+    if (dy_dtype == SDM_BF16) launch_norm_grad<bf16, bf16>(p, grid, a, st);
+    else launch_norm_grad<bf16, float>(p, grid, a, st);
+  } else {
+    if (dy_dtype == SDM_BF16) launch_norm_grad<float, bf16>(p, grid, a, st);
+    else launch_norm_grad<float, float>(p, grid, a, st);
+  }
+  if ((r = launch_status("rmsnorm_residual_backward launch")) != SDM_OK) return r;
+  sdm::k_sum_slots<<<(d + 31) / 32, dim3(32, 32), 0, st>>>(part, static_cast<int64_t>(grid) * p.rpb, d, dw);
+  if ((r = launch_status("dw sum launch")) != SDM_OK) return r;
+  return ok();
+}
+
+}  // extern "C"

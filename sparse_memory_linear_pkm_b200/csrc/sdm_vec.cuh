@@ -1,0 +1,82 @@
+// Loads and stores of a few consecutive values as fp32 (sm_100a).
+#pragma once
+
+#include "sdm_device.cuh"
+
+namespace sdm {
+
+// V consecutive values of T as fp32; V > 1 is one aligned access of 4 to 16
+// bytes (16-bit types: 2, 4 or 8 values, fp32: 2 or 4).
+template <typename T, int V>
+__device__ __forceinline__ void load_unit(const T* p, float* v) {
+  if constexpr (V == 1) {
+    v[0] = to_f32<T>(*p);
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x; v[1] = f.y;
+  } else if constexpr (sizeof(T) == 4) {
+    static_assert(V == 4, "fp32 units hold two or four values");
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    static_assert(V == 2 || V == 4 || V == 8, "16-bit units hold two, four or eight values");
+    uint32_t q[V / 2];
+    if constexpr (V == 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      q[0] = u.x; q[1] = u.y; q[2] = u.z; q[3] = u.w;
+    } else if constexpr (V == 4) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      q[0] = u.x; q[1] = u.y;
+    } else {
+      q[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      v[2 * i] = __uint_as_float(q[i] << 16);
+      v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_unit(T* p, const float* v) {
+  if constexpr (V == 1) {
+    *p = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t q[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      q[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+    else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(p) = q[0];
+  }
+}
+
+// Eight consecutive values (16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    load_unit<T, 4>(p, v);
+    load_unit<T, 4>(p + 4, v + 4);
+  } else {
+    load_unit<T, 8>(p, v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    store_unit<T, 4>(p, v);
+    store_unit<T, 4>(p + 4, v + 4);
+  } else {
+    store_unit<T, 8>(p, v);
+  }
+}
+
+}  // namespace sdm
