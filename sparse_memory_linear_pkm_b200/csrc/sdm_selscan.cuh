@@ -7,20 +7,22 @@
 //
 // What bounds it: one exponential per (token, channel, state). An SM makes 16 a
 // clock, so N = 16 states cost a clock per (token, channel) on each SM, three
-// times what the 8 bytes of a bf16 (token, channel) cost in HBM time. The
-// kernel therefore makes each exponential once and keeps it.
+// times what the 8 bytes of a bf16 (token, channel) cost in HBM time. All else
+// is kept below that: a lane holds one channel with KS states in registers (N >
+// KS: L lanes share a channel), so the step size, the input and the gate are
+// computed where they are used and the sum over n stays in the lane; B and C
+// are the same for all lanes and come as fp32 from shared memory, where loads
+// that neighbouring lanes share cost half; two states take one packed fp32
+// instruction. (Lanes that held four states each spent their time on shared
+// memory and on exchanging sums: 2.1 ms instead of 0.9 for B = 8, T = 4096, D =
+// 4096, N = 16 in bf16.)
 //
-// Layout: a lane holds four states of one channel, L lanes a channel, so a warp
-// holds 32 / L channels and the sum over n takes log2 L exchanges, which are
-// shared between L tokens (each lane ends with the sum of another token). A
-// block holds CG such channel groups; its W warps along time hold consecutive
-// segments of S tokens, with the segment's exponentials in registers: each warp
-// first runs its segment from zero, the segments' maps (h -> P h + H) are
-// joined in shared memory, and each warp runs its segment again from the right
-// state with the exponentials it kept. With W = 1 there is one pass.
+// The tokens of a split are walked in order. Where the channels alone do not
+// fill the device, the token axis is split: a first launch runs each split from
+// a zero state and keeps its map h -> P h + H, k_selective_scan_join chains the
+// maps, and the second launch starts each split from its state.
 //
-// Tokens past a sequence's length have delta = 0 and B = C = 0: the state
-// passes through them unchanged and nothing of their rows is read.
+// Tokens past a sequence's length are not read.
 #pragma once
 
 #include "sdm_conv.cuh"
@@ -30,7 +32,6 @@
 namespace sdm {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLog2eLow = 1.92596299112661746887e-8f;  // log2(e) - fp32(log2(e))
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct SelScanArgs {
@@ -46,20 +47,19 @@ struct SelScanArgs {
   const float* h_in;       // initial states (nullptr: zeros); see in_splits
   float* h_out;            // final states [B, D, N] or nullptr
   void* y;                 // [B, T, D]
-  float* sums;             // kSelSums: decays, then states [B, splits, D, N]
-  float* ckpt;             // kSelCkpt: state before each tile [B, tiles, D, N]
+  float* sums;             // kSelSums: the splits' decays, then their states [B, splits, D, N]
   int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
   int T, D, N, G;
   int tiles_per_group;     // channel tiles of one group of D / G channels
   int splits;              // parts of the token axis
   int in_splits;           // h_in holds one state per split ([B, splits, D, N])
-  int tokens_per_split;    // a multiple of the tile
+  int tokens_per_split;
   int softplus;
-  int vec_x, vec_b;        // channel rows / B and C rows are whole aligned units
+  int vec_x, vec_b;        // rows of channels / of B and C are whole aligned units of four
   unsigned* err;
 };
 
-enum SelMode { kSelRun = 0, kSelSums = 1, kSelCkpt = 2 };
+enum SelMode { kSelRun = 0, kSelSums = 1 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -67,47 +67,43 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// exp(u) with the rounding error of u * log2(e) put back.
-__device__ __forceinline__ float exp_full(float u) {
-  const float t = u * kLog2e;
-  const float low = fmaf(u, kLog2eLow, fmaf(u, kLog2e, -t));
-  const float e = ex2(t);
-  return fmaf(e, low * kLn2, e);
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-
-// softplus(u) = max(u, 0) + log(1 + e), e = exp(-|u|) in (0, 1], by the series
-// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: through s^15 the remainder
-// is below 2e-9 relative. Small values keep their relative accuracy.
-__device__ __forceinline__ float softplus(float u) {
-  const float e = exp_full(-fabsf(u));
-  const float s = __fdividef(e, 2.0f + e), q = s * s;
-  float p = 1.0f / 15.0f;
-  p = fmaf(p, q, 1.0f / 13.0f);
-  p = fmaf(p, q, 1.0f / 11.0f);
-  p = fmaf(p, q, 1.0f / 9.0f);
-  p = fmaf(p, q, 1.0f / 7.0f);
-  p = fmaf(p, q, 1.0f / 5.0f);
-  p = fmaf(p, q, 1.0f / 3.0f);
-  p = fmaf(p, q, 1.0f);
-  return fmaxf(u, 0.0f) + 2.0f * s * p;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
+      " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 low2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 high2(float4 v) { return make_float2(v.z, v.w); }
 
-// Sums over the L lanes of each channel (lane bits below log2 L) of L values:
-// lane j (of a channel) returns the total of v[j].
-template <int L>
-__device__ __forceinline__ float sum_to_lane(float (&v)[L]) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o];
-      const float keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
+// softplus of two values: max(u, 0) + log(1 + e), e = exp(-|u|) in (0, 1], with
+// log(1 + e) = e q(e). q is the polynomial of degree 8 with the least relative
+// error on [0, 1] (3e-8, fitted by reweighted least squares at Chebyshev
+// points), so that small results keep their relative accuracy.
+__device__ __forceinline__ float2 softplus2(float2 u) {
+  const float2 e = make_float2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
+  float2 q = both(0.0052326880395412445f);
+  q = fma2(q, e, both(-0.029505213722586632f));
+  q = fma2(q, e, both(0.07822591066360474f));
+  q = fma2(q, e, both(-0.13663242757320404f));
+  q = fma2(q, e, both(0.19106005132198334f));
+  q = fma2(q, e, both(-0.2484298199415207f));
+  q = fma2(q, e, both(0.3331909775733948f));
+  q = fma2(q, e, both(-0.4999949336051941f));
+  q = fma2(q, e, both(0.9999999403953552f));
+  return fma2(e, q, make_float2(fmaxf(u.x, 0.0f), fmaxf(u.y, 0.0f)));
 }
 
 // V channels of token row p, of which `n` exist; zeros elsewhere.
@@ -120,6 +116,7 @@ __device__ __forceinline__ void load_channels(const T* p, bool vec, int n, float
     for (int i = 0; i < V; ++i) v[i] = i < n ? to_f32<T>(p[i]) : 0.f;
   }
 }
+
 template <typename T, int V>
 __device__ __forceinline__ void store_channels(T* p, bool vec, int n, const float* v) {
   if (vec && n >= V) {
@@ -155,243 +152,222 @@ __device__ __forceinline__ void store_states(float* row, int n, int N, const flo
   }
 }
 
-template <int L, int S, int W, int CG>
-struct SelTile {
-  static constexpr int kThreads = 32 * W * CG;
-  static constexpr int NP = 4 * L;             // states a channel is padded to
-  static constexpr int CW = 32 / L;            // channels of a warp
-  static constexpr int CH = CW * CG;           // channels of a block
-  static constexpr int TT = S * W;             // tokens of a tile
-  static constexpr int I = S / L;              // (token, channel) items per thread
-  static constexpr int V = I >= 4 ? 4 : (I >= 2 ? 2 : 1);
-  static constexpr int UR = CH / V;            // channel units of a token row
-  static constexpr int U = (TT * UR + kThreads - 1) / kThreads;
-  static constexpr int UB = (TT * L + kThreads - 1) / kThreads;  // 4-state units of B (and of C)
-  // Shared memory: (delta, delta x) pairs, B, C, y sums, segment maps, carried state.
-  static constexpr int kSmemFloats =
-      2 * TT * CH + 2 * TT * NP + TT * CH + (W > 1 ? 2 * W * CH * NP : 0) + CH * NP;
+constexpr int kSelThreads = 128;
+constexpr int kSelTile = 16;   // tokens of B and C staged at a time
+constexpr int kSelAhead = 4;   // tokens whose x, dt and z are loaded together, one such run ahead
+
+// A 16- or 32-bit value as loaded, so that nothing waits for the load before
+// the value is used.
+template <typename T>
+struct RawOne;
+template <>
+struct RawOne<float> {
+  float v;
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ float get() const { return v; }
+};
+template <>
+struct RawOne<bf16> {
+  uint16_t v;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint16_t*>(p); }
+  __device__ __forceinline__ float get() const { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 };
 
-template <typename T, int L, int S, int W, int CG, int kMode>
-__global__ void __launch_bounds__(32 * W * CG) k_selective_scan(const SelScanArgs a) {
-  static_assert(kMode == kSelRun || W > 1, "the modes without outputs run on segment maps");
-  static_assert(S % L == 0, "sums are exchanged for L tokens at a time");
-  using Tile = SelTile<L, S, W, CG>;
-  constexpr int NP = Tile::NP, CW = Tile::CW, CH = Tile::CH, TT = Tile::TT, V = Tile::V;
-  extern __shared__ float4 smem4[];
-  float2* s_dx = reinterpret_cast<float2*>(smem4);                  // [TT][CH]
-  float* s_B = reinterpret_cast<float*>(s_dx + TT * CH);            // [TT][NP]
-  float* s_C = s_B + TT * NP;                                       // [TT][NP]
-  float* s_y = s_C + TT * NP;                                       // [TT][CH]
-  float* s_h = s_y + TT * CH;                                       // [CH][NP] state before the tile
-  float* s_P = s_h + CH * NP;                                       // [W][CH][NP]
-  float* s_H = s_P + W * CH * NP;                                   // [W][CH][NP]
+// Four values of B or C likewise, of which `n` exist (zeros else).
+template <typename T>
+struct Raw4 {
+  uint32_t w[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p, bool vec, int n) {
+    if (vec && n >= 4) {
+      if constexpr (sizeof(T) == 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        w[0] = q.x; w[1] = q.y;
+      }
+      return;
+    }
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0u;
+      if (i < n) v[i] = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(p)[i] : reinterpret_cast<const uint16_t*>(p)[i];
+    }
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) w[i] = sizeof(T) == 4 ? v[i] : v[(2 * i) & 3] | v[(2 * i + 1) & 3] << 16;
+  }
+  __device__ __forceinline__ float4 get() const {
+    if constexpr (sizeof(T) == 4)
+      return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+    else
+      return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                         __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u));
+  }
+};
 
-  const int tid = threadIdx.x, lane = lane_id(), warp = tid / kWarp;
-  const int wt = warp % W, cg = warp / W;
+// KS states a lane, L lanes a channel; blocks of kSelThreads / L channels.
+template <typename T, int KS, int L, int kMode>
+__global__ void __launch_bounds__(kSelThreads) k_selective_scan(const SelScanArgs a) {
+  constexpr int NP = KS * L, CH = kSelThreads / L, KP = KS / 2;
+  constexpr int kUnits = kSelTile * NP / 4;  // 4-state units of a tile of B (or C)
+  constexpr int UB = (kUnits + kSelThreads - 1) / kSelThreads;
+  __shared__ float4 s_B[2][kUnits], s_C[kMode == kSelRun ? 2 : 1][kMode == kSelRun ? kUnits : 1];
+
+  const int tid = threadIdx.x;
   const int split = blockIdx.y, b = blockIdx.z;
   const int group = blockIdx.x / a.tiles_per_group, tile_c = blockIdx.x % a.tiles_per_group;
-  const int Dg = a.D / a.G, c0 = group * Dg + tile_c * CH, c_end = (group + 1) * Dg;
+  const int Dg = a.D / a.G, c_end = (group + 1) * Dg;
   const int len = clamp_length(a.lengths, b, a.T, a.err);
   const int t_begin = split * a.tokens_per_split;
-  const int t_end = min(min(a.T, len), t_begin + a.tokens_per_split);
+  const int t_end = min(len, t_begin + a.tokens_per_split);
 
-  // This lane's channel and states.
-  const int ch = cg * CW + lane / L, n0 = 4 * (lane % L);
-  const bool live = c0 + ch < c_end;
-  const int64_t c = live ? c0 + ch : c0;
-  float A2[4], h[4];
-  load_states(a.A + c * a.N, n0, a.N, A2);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) A2[k] *= kLog2e, h[k] = 0.f;
-  if (a.h_in != nullptr) {
+  // This lane's channel (the last one again where there is none) and states.
+  const int c_want = group * Dg + tile_c * CH + tid / L, c = min(c_want, c_end - 1);
+  const bool live = c_want < c_end, writes = live && tid % L == 0;
+  const int n0 = (tid % L) * KS;
+  float2 A2[KP], h[KP];
+  {
     const int64_t row = a.in_splits ? static_cast<int64_t>(b) * a.splits + split : b;
-    load_states(a.h_in + (row * a.D + c) * a.N, n0, a.N, h);
+#pragma unroll
+    for (int k = 0; k < KP; k += 2) {
+      float v[4];
+      load_states(a.A + static_cast<int64_t>(c) * a.N, n0 + 2 * k, a.N, v);
+      A2[k] = mul2(make_float2(v[0], v[1]), both(kLog2e));
+      A2[k + 1] = mul2(make_float2(v[2], v[3]), both(kLog2e));
+      v[0] = v[1] = v[2] = v[3] = 0.f;
+      if (a.h_in != nullptr) load_states(a.h_in + (row * a.D + c) * a.N, n0 + 2 * k, a.N, v);
+      h[k] = make_float2(v[0], v[1]);
+      h[k + 1] = make_float2(v[2], v[3]);
+    }
   }
-  if (kMode == kSelRun && W > 1 && wt == 0)
-    *reinterpret_cast<float4*>(s_h + ch * NP + n0) = make_float4(h[0], h[1], h[2], h[3]);
-  float decay = 0.f;  // kSelSums: the segment warps' sum of delta
+  const float bias = a.bias == nullptr ? 0.f : a.bias[c], skip = a.Dskip == nullptr ? 0.f : a.Dskip[c];
+  const bool gated = kMode == kSelRun && a.z != nullptr;
+  float total = 0.f;  // kSelSums: sum of delta
 
-  const T* gx = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride;
-  const T* gdt = static_cast<const T*>(a.dt) + static_cast<int64_t>(b) * a.T * a.dt_stride;
-  const T* gz = a.z == nullptr ? nullptr : static_cast<const T*>(a.z) + static_cast<int64_t>(b) * a.T * a.z_stride;
-  const T* gB = static_cast<const T*>(a.Bm) + static_cast<int64_t>(b) * a.T * a.b_stride + group * a.N;
-  const T* gC = static_cast<const T*>(a.Cm) + static_cast<int64_t>(b) * a.T * a.c_stride + group * a.N;
-  T* gy = static_cast<T*>(a.y) + static_cast<int64_t>(b) * a.T * a.D;
+  const int64_t row0 = static_cast<int64_t>(b) * a.T + t_begin;
+  const T* gx = static_cast<const T*>(a.x) + row0 * a.x_stride + c;
+  const T* gd = static_cast<const T*>(a.dt) + row0 * a.dt_stride + c;
+  const T* gz = gated ? static_cast<const T*>(a.z) + row0 * a.z_stride + c : nullptr;
+  const T* gB = static_cast<const T*>(a.Bm) + row0 * a.b_stride + group * a.N;
+  const T* gC = static_cast<const T*>(a.Cm) + row0 * a.c_stride + group * a.N;
+  T* gy = static_cast<T*>(a.y) + row0 * a.D + c;
 
-  // Values of the next tile, loaded while this one is computed.
-  float px[Tile::U][V], pd[Tile::U][V], pz[Tile::U][V], pB[Tile::UB][4], pC[Tile::UB][4];
+  // B and C of a tile: loaded a tile before they are written to shared memory.
+  Raw4<T> rB[UB], rC[UB];
   auto fetch = [&](int t0) {
 #pragma unroll
-    for (int u = 0; u < Tile::U; ++u) {
-      const int i = tid + u * Tile::kThreads, t = t0 + i / Tile::UR, cc = c0 + (i % Tile::UR) * V;
-      const int n = (i < TT * Tile::UR && t < t_end) ? c_end - cc : 0;
-      load_channels<T, V>(gx + t * a.x_stride + cc, a.vec_x, n, px[u]);
-      load_channels<T, V>(gdt + t * a.dt_stride + cc, a.vec_x, n, pd[u]);
-      if (kMode == kSelRun && gz != nullptr) load_channels<T, V>(gz + t * a.z_stride + cc, a.vec_x, n, pz[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < Tile::UB; ++u) {
-      const int i = tid + u * Tile::kThreads, t = t0 + i / L, n = (i % L) * 4;
-      const int left = (i < TT * L && t < t_end) ? a.N - n : 0;
-      load_channels<T, 4>(gB + t * a.b_stride + n, a.vec_b, left, pB[u]);
-      if (kMode == kSelRun) load_channels<T, 4>(gC + t * a.c_stride + n, a.vec_b, left, pC[u]);
+    for (int u = 0; u < UB; ++u) {
+      const int i = tid + u * kSelThreads, r = i / (NP / 4), n = i % (NP / 4) * 4;
+      const int left = (kUnits % kSelThreads == 0 || i < kUnits) && t0 + r < t_end ? a.N - n : 0;
+      const int64_t t = t0 - t_begin + r;
+      rB[u].load(gB + t * a.b_stride + n, a.vec_b, left);
+      if (kMode == kSelRun) rC[u].load(gC + t * a.c_stride + n, a.vec_b, left);
     }
   };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < UB; ++u) {
+      const int i = tid + u * kSelThreads;
+      if (kUnits % kSelThreads == 0 || i < kUnits) {
+        s_B[buf][i] = rB[u].get();
+        if (kMode == kSelRun) s_C[buf][i] = rC[u].get();
+      }
+    }
+  };
+  // x, dt and z of the next kSelAhead tokens, all loaded and all used together:
+  // a wait for one load is a wait for every load still on its way.
+  RawOne<T> rx[kSelAhead], rd[kSelAhead], rz[kSelAhead];
+  auto ahead = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kSelAhead; ++i) {
+      if (t + i < t_end) {
+        rx[i].load(gx + i * a.x_stride);
+        rd[i].load(gd + i * a.dt_stride);
+        if (gated) rz[i].load(gz + i * a.z_stride);
+      }
+    }
+    gx += kSelAhead * a.x_stride;
+    gd += kSelAhead * a.dt_stride;
+    if (gated) gz += kSelAhead * a.z_stride;
+  };
+  ahead(t_begin);
   fetch(t_begin);
-
-  for (int t0 = t_begin; t0 < t_end; t0 += TT) {
-    // Stage the tile: step sizes and scaled inputs per channel, B and C as fp32.
-    float x[Tile::U][V], z[Tile::U][V];
+  stage(0);
+  fetch(t_begin + kSelTile);
+  int buf = 0;
+  for (int t0 = t_begin; t0 < t_end; t0 += kSelTile, buf ^= 1) {
+    __syncthreads();  // this tile is staged, and nobody reads the buffer of the next one any more
+    stage(buf ^ 1);
+    fetch(t0 + 2 * kSelTile);
+    const float4* sB = s_B[buf] + n0 / 4;
+    const float4* sC = s_C[kMode == kSelRun ? buf : 0] + n0 / 4;
+    for (int t1 = t0; t1 < min(t0 + kSelTile, t_end); t1 += kSelAhead) {
+      float x[kSelAhead], d[kSelAhead], gate[kSelAhead];
 #pragma unroll
-    for (int u = 0; u < Tile::U; ++u) {
-      const int i = tid + u * Tile::kThreads, tt = i / Tile::UR, cc = (i % Tile::UR) * V;
+      for (int i = 0; i < kSelAhead; i += 2) {
+        float2 p = make_float2(rd[i].get() + bias, rd[i + 1].get() + bias);
+        if (a.softplus) p = softplus2(p);
+        d[i] = t1 + i < t_end ? p.x : 0.f;  // a step of 0 leaves the state as it is
+        d[i + 1] = t1 + i + 1 < t_end ? p.y : 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[u][v] = px[u][v];
-        if (kMode == kSelRun) z[u][v] = pz[u][v];
-        float d = 0.f;
-        if (t0 + tt < t_end && c0 + cc + v < c_end) {
-          d = pd[u][v] + (a.bias == nullptr ? 0.f : a.bias[c0 + cc + v]);
-          if (a.softplus) d = softplus(d);
-        }
-        if (i < TT * Tile::UR) s_dx[tt * CH + cc + v] = make_float2(d, d * x[u][v]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < Tile::UB; ++u) {
-      const int i = tid + u * Tile::kThreads;
-      if (i < TT * L) {
-        *reinterpret_cast<float4*>(s_B + i * 4) = make_float4(pB[u][0], pB[u][1], pB[u][2], pB[u][3]);
-        if (kMode == kSelRun)
-          *reinterpret_cast<float4*>(s_C + i * 4) = make_float4(pC[u][0], pC[u][1], pC[u][2], pC[u][3]);
-      }
-    }
-    if (kMode == kSelCkpt && wt == 0) {
-      // h holds the state before the tile in these warps.
-      const int64_t row = static_cast<int64_t>(b) * ((a.T + TT - 1) / TT) + t0 / TT;
-      if (live) store_states(a.ckpt + (row * a.D + c) * a.N, n0, a.N, h);
-    }
-    __syncthreads();
-    fetch(t0 + TT);
-
-    const float2* dx = s_dx + wt * S * CH + ch;
-    const float4* Bs = reinterpret_cast<const float4*>(s_B + wt * S * NP + n0);
-    const float4* Cs = reinterpret_cast<const float4*>(s_C + wt * S * NP + n0);
-    float e[W > 1 ? S : 1][4];
-    if constexpr (W > 1) {
-      // The segment from a zero state.
-      float H[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const float2 d = dx[s * CH];
-        const float4 Bv = Bs[s * L];
-        const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w};
-        sum += d.x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e[s][k] = ex2(d.x * A2[k]);
-          H[k] = fmaf(e[s][k], H[k], d.y * Bk[k]);
+        for (int j = i; j < i + 2; ++j) {
+          x[j] = t1 + j < t_end ? rx[j].get() : 0.f;
+          gate[j] = gated ? silu_fast(rz[j].get()) : 1.0f;
         }
       }
-      const int at = (wt * CH + ch) * NP + n0;
-      *reinterpret_cast<float4*>(s_P + at) =
-          make_float4(ex2(sum * A2[0]), ex2(sum * A2[1]), ex2(sum * A2[2]), ex2(sum * A2[3]));
-      *reinterpret_cast<float4*>(s_H + at) = make_float4(H[0], H[1], H[2], H[3]);
-      if (kMode == kSelSums) decay += sum;
-      __syncthreads();
-      // The state before this warp's segment. In the modes without outputs only
-      // the state after the tile is wanted; the group's first warp carries it.
-      if (kMode == kSelRun) {
-        const float4 h0 = *reinterpret_cast<const float4*>(s_h + ch * NP + n0);
-        h[0] = h0.x; h[1] = h0.y; h[2] = h0.z; h[3] = h0.w;
-      }
-      const int upto = kMode == kSelRun ? wt : (wt == 0 ? W : 0);
-      for (int v = 0; v < upto; ++v) {
-        const float4 p = *reinterpret_cast<const float4*>(s_P + (v * CH + ch) * NP + n0);
-        const float4 q = *reinterpret_cast<const float4*>(s_H + (v * CH + ch) * NP + n0);
-        h[0] = fmaf(p.x, h[0], q.x);
-        h[1] = fmaf(p.y, h[1], q.y);
-        h[2] = fmaf(p.z, h[2], q.z);
-        h[3] = fmaf(p.w, h[3], q.w);
-      }
-    }
-    if constexpr (kMode == kSelRun) {
+      ahead(t1 + kSelAhead);
 #pragma unroll
-      for (int s0 = 0; s0 < S; s0 += L) {
-        float sums[L];
+      for (int i = 0; i < kSelAhead; ++i) {
+        const float2 dd = both(d[i]), w = both(d[i] * x[i]);
+        float2 y[2] = {both(0.f), both(0.f)};
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-          const int s = s0 + j;
-          const float2 d = dx[s * CH];
-          const float4 Bv = Bs[s * L], Cv = Cs[s * L];
-          const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, Ck[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
-          float y = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float ek = W > 1 ? e[W > 1 ? s : 0][k] : ex2(d.x * A2[k]);
-            h[k] = fmaf(ek, h[k], d.y * Bk[k]);
-            y = fmaf(Ck[k], h[k], y);
+        for (int k = 0; k < KP; k += 2) {
+          const float4 Bv = sB[i * (NP / 4) + k / 2];
+          const float2 p0 = mul2(dd, A2[k]), p1 = mul2(dd, A2[k + 1]);
+          h[k] = fma2(make_float2(ex2(p0.x), ex2(p0.y)), h[k], mul2(w, low2(Bv)));
+          h[k + 1] = fma2(make_float2(ex2(p1.x), ex2(p1.y)), h[k + 1], mul2(w, high2(Bv)));
+          if (kMode == kSelRun) {
+            const float4 Cv = sC[i * (NP / 4) + k / 2];
+            y[0] = fma2(low2(Cv), h[k], y[0]);
+            y[1] = fma2(high2(Cv), h[k + 1], y[1]);
           }
-          sums[j] = y;
         }
-        const float y = sum_to_lane<L>(sums);
-        s_y[(wt * S + s0 + lane % L) * CH + ch] = y;
-      }
-    }
-    if constexpr (kMode == kSelRun) {
-      __syncthreads();
-      // The last segment's end is the state before the next tile; every warp
-      // has read the one before this tile.
-      if (W > 1 && wt == W - 1) *reinterpret_cast<float4*>(s_h + ch * NP + n0) = make_float4(h[0], h[1], h[2], h[3]);
+        if (kMode == kSelRun) {
+          float o = (y[0].x + y[0].y) + (y[1].x + y[1].y);
 #pragma unroll
-      for (int u = 0; u < Tile::U; ++u) {
-        const int i = tid + u * Tile::kThreads, tt = i / Tile::UR, cc = (i % Tile::UR) * V;
-        const int t = t0 + tt;
-        const int n = (i < TT * Tile::UR && t < t_end) ? c_end - (c0 + cc) : 0;
-        if (n > 0) {
-          float o[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            o[v] = s_y[tt * CH + cc + v];
-            if (a.Dskip != nullptr && v < n) o[v] = fmaf(a.Dskip[c0 + cc + v], x[u][v], o[v]);
-            if (gz != nullptr) o[v] *= silu_fast(z[u][v]);
-          }
-          store_channels<T, V>(gy + static_cast<int64_t>(t) * a.D + c0 + cc, a.vec_x, n, o);
+          for (int q = L / 2; q > 0; q >>= 1) o += __shfl_xor_sync(0xffffffffu, o, q);
+          o = fmaf(skip, x[i], o) * gate[i];
+          if (writes && t1 + i < t_end) gy[i * static_cast<int64_t>(a.D)] = from_f32<T>(o);
+        } else {
+          total += d[i];
         }
       }
+      sB += kSelAhead * (NP / 4);
+      sC += kSelAhead * (NP / 4);
+      gy += kSelAhead * static_cast<int64_t>(a.D);
     }
   }
-  // The final state: in every warp with W = 1, else in the group's last warp
-  // (kSelRun) or first warp.
-  const bool has = W == 1 || (kMode == kSelRun ? wt == W - 1 : wt == 0);
+  if (!live) return;
+  float* out = a.h_out == nullptr || split != a.splits - 1
+                   ? nullptr
+                   : a.h_out + (static_cast<int64_t>(b) * a.D + c) * a.N;
   if (kMode == kSelSums) {
-    // Decay of the whole split from the sum of its step sizes.
-    const int64_t row = (static_cast<int64_t>(b) * a.splits + split) * a.D + c;
-    const int64_t all = static_cast<int64_t>(gridDim.z) * a.splits * a.D * a.N;
-    if (W > 1) {
-      __syncthreads();
-      if (n0 == 0) s_y[wt * CH + ch] = decay;
-      __syncthreads();
-      decay = 0.f;
-      for (int v = 0; v < W; ++v) decay += s_y[v * CH + ch];
-    }
-    if (has && live) {
-      float P[4];
+    const int64_t at = ((static_cast<int64_t>(b) * a.splits + split) * a.D + c) * a.N;
+    out = a.sums + static_cast<int64_t>(gridDim.z) * a.splits * a.D * a.N + at;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) P[k] = ex2(decay * A2[k]);
-      store_states(a.sums + row * a.N, n0, a.N, P);
-      store_states(a.sums + all + row * a.N, n0, a.N, h);
+    for (int k = 0; k < KP; k += 2) {
+      const float2 p0 = mul2(both(total), A2[k]), p1 = mul2(both(total), A2[k + 1]);
+      const float P[4] = {ex2(p0.x), ex2(p0.y), ex2(p1.x), ex2(p1.y)};
+      store_states(a.sums + at, n0 + 2 * k, a.N, P);
     }
-  } else if (a.h_out != nullptr && has && live && split == a.splits - 1) {
-    if (W > 1 && t_begin >= t_end) {
-      // No token: warp W - 1 never took the state from shared memory.
-      const int64_t row = a.in_splits ? static_cast<int64_t>(b) * a.splits + split : b;
+  }
+  if (out != nullptr) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = 0.f;
-      if (a.h_in != nullptr) load_states(a.h_in + (row * a.D + c) * a.N, n0, a.N, h);
+    for (int k = 0; k < KP; k += 2) {
+      const float v[4] = {h[k].x, h[k].y, h[k + 1].x, h[k + 1].y};
+      store_states(out, n0 + 2 * k, a.N, v);
     }
-    store_states(a.h_out + (static_cast<int64_t>(b) * a.D + c) * a.N, n0, a.N, h);
   }
 }
 
@@ -404,11 +380,20 @@ static __global__ void __launch_bounds__(256) k_selective_scan_join(const float*
   if (i >= total) return;
   const int64_t b = i / per_b, r = i % per_b;
   float h = h0 == nullptr ? 0.f : h0[i];
-  for (int s = 0; s < splits; ++s) {
-    const int64_t at = (b * splits + s) * per_b + r;
-    const float p = P[at], q = H[at];
-    H[at] = h;
-    h = fmaf(p, h, q);
+  constexpr int kAhead = 8;  // the loads of as many splits go out together
+  for (int s0 = 0; s0 < splits; s0 += kAhead) {
+    const int64_t at = (b * splits + s0) * per_b + r;
+    float p[kAhead], q[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      p[j] = s0 + j < splits ? P[at + j * per_b] : 0.f;
+      q[j] = s0 + j < splits ? H[at + j * per_b] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s0 + j < splits) H[at + j * per_b] = h;
+      h = fmaf(p[j], h, q[j]);
+    }
   }
 }
 
@@ -437,7 +422,7 @@ __global__ void __launch_bounds__(256) k_selective_scan_step(const SelScanArgs a
       x = to_f32<T>(static_cast<const T*>(a.x)[tok * a.x_stride + c]);
       d = to_f32<T>(static_cast<const T*>(a.dt)[tok * a.dt_stride + c]) + bias;
       if (a.z != nullptr) z = to_f32<T>(static_cast<const T*>(a.z)[tok * a.z_stride + c]);
-      if (a.softplus) d = softplus(d);
+      if (a.softplus) d = softplus2(both(d)).x;
     }
     load_channels<T, 4>(static_cast<const T*>(a.Bm) + tok * a.b_stride + g * a.N + n0, a.vec_b, on ? a.N - n0 : 0, Bk);
     load_channels<T, 4>(static_cast<const T*>(a.Cm) + tok * a.c_stride + g * a.N + n0, a.vec_b, on ? a.N - n0 : 0, Ck);

@@ -9,10 +9,10 @@
 //   ddt_t = ddelta_t sigmoid(dt_t + bias),  dbias = sum_t ddt_t
 //   dz_t  = dy_t (C_t.h_t + D x_t) silu'(z_t)
 //
-// h is not kept by the forward: a first kernel (k_selective_scan, kSelCkpt)
-// stores the state before every tile of tokens, and this one walks the tiles
-// from the last to the first. Within a tile the layout is the forward's: warps
-// along time hold segments with their exponentials (and u) in registers. One
+// h is not kept by the forward: its first two launches on splits of one tile
+// give the state before every tile of tokens, and this one walks the tiles from
+// the last to the first. A lane holds four states of one channel; warps along
+// time hold segments with their exponentials (and u) in registers. One
 // run over a segment gives its maps in both directions, h -> P h + H and
 // q -> P q + Q, which a thread per (channel, state) chains over the segments.
 //
@@ -26,7 +26,8 @@
 namespace sdm {
 
 struct SelGradArgs {
-  SelScanArgs f;          // the forward's inputs; f.ckpt: states before the tiles
+  SelScanArgs f;          // the forward's inputs
+  const float* ckpt;      // states before the tiles [B, tiles, D, N]
   const void* dy;         // [B, T, D]
   const float* dstate;    // dL/dh_T [B, D, N] or nullptr
   void* dx;               // [B, T, D]
@@ -39,6 +40,38 @@ struct SelGradArgs {
   float* part_bias;       // [B, D]
   float* dstate0;         // [B, D, N] or nullptr
 };
+
+template <int L, int S, int W, int CG>
+struct SelTile {
+  static constexpr int kThreads = 32 * W * CG;
+  static constexpr int NP = 4 * L;             // states a channel is padded to
+  static constexpr int CW = 32 / L;            // channels of a warp
+  static constexpr int CH = CW * CG;           // channels of a block
+  static constexpr int TT = S * W;             // tokens of a tile
+  static constexpr int I = S / L;              // (token, channel) items per thread
+  static constexpr int V = I >= 4 ? 4 : (I >= 2 ? 2 : 1);
+  static constexpr int UR = CH / V;            // channel units of a token row
+  static constexpr int U = (TT * UR + kThreads - 1) / kThreads;
+  static constexpr int UB = (TT * L + kThreads - 1) / kThreads;  // 4-state units of B (and of C)
+};
+
+// Sums over the L lanes of each channel (lane bits below log2 L) of L values:
+// lane j (of a channel) returns the total of v[j].
+template <int L>
+__device__ __forceinline__ float sum_to_lane(float (&v)[L]) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o];
+      const float keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
 
 template <int L, int S, int W, int CG>
 struct SelGradTile : SelTile<L, S, W, CG> {
@@ -156,7 +189,7 @@ __global__ void __launch_bounds__(32 * W * CG) k_selective_scan_backward(const S
       ph[j] = 0.f;
       if (tile >= 0 && t0 < len && i < kPairs) {
         const int64_t at = pair_at(static_cast<int64_t>(b) * tiles + tile, i);
-        if (at >= 0) ph[j] = a.ckpt[at];
+        if (at >= 0) ph[j] = ga.ckpt[at];
       }
     }
   };
@@ -212,7 +245,7 @@ __global__ void __launch_bounds__(32 * W * CG) k_selective_scan_backward(const S
         z[u][v] = gz != nullptr ? pz[u][v] : 0.f;
         pre[u][v] = pd[u][v] + bias[v];
         float d = 0.f;
-        if (t0 + tt < len && c0 + my_c + v < c_end) d = a.softplus ? softplus(pre[u][v]) : pre[u][v];
+        if (t0 + tt < len && c0 + my_c + v < c_end) d = a.softplus ? softplus2(both(pre[u][v])).x : pre[u][v];
         if (i < TT * UR) {
           s_dx[tt * CH + my_c + v] = make_float2(d, d * x[u][v]);
           s_e[tt * CH + my_c + v] = gz != nullptr ? dy[u][v] * silu_fast(z[u][v]) : dy[u][v];

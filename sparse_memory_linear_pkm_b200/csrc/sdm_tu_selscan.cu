@@ -6,88 +6,81 @@ namespace sdm_host {
 
 namespace {
 
-// Tokens a sequence may have for the kernel that keeps nothing but the state's
-// four values per thread: there its tokens are a serial chain of loads.
+// Tokens a sequence may have for the kernel that keeps nothing but four states
+// a thread: there its tokens are a serial chain of loads.
 constexpr int kStepTokens = 4;
+// A split of the token axis has at least this many tokens: its map costs the
+// bandwidth of about 30.
+constexpr int kSplitTokens = 128;
 
 struct SelPlan {
-  bool step = false, one_pass = false;
-  int ch = 0;               // channels of a block
+  bool step = false;
   int splits = 1, tokens_per_split = 0;
-  size_t state_bytes = 0;   // one [B, splits, D, N] fp32 array
+  size_t state_bytes = 0;  // one [B, splits, D, N] fp32 array
 };
 
-// Three ways, by how many channels there are to fill 148 SMs with:
-//   - many (W = 1): a block takes 64-odd channels and walks the tokens once;
-//   - few (W = 8): a block takes an eighth of that and eight warps share the
-//     tokens of a tile, at the cost of a second run over each segment;
-//   - very few, and a long sequence: the token axis is split over blocks as
-//     well, whose maps are joined in between (each exponential twice).
+// Splitting makes every exponential twice, so it pays where the channels leave
+// most of the device idle: with w warps an SM one pass takes about 1.14 / w
+// clocks per exponential (0.41 at 2.6, 0.165 at 6.9), two take 0.19 once some
+// 30 warps an SM are there (0.178 at B = 8, T = 4096, D = 4096; 0.198 at B = 1,
+// T = 16384, D = 2048).
 SelPlan sel_plan(const sdm_selscan_shape_t& s) {
   SelPlan p;
-  if (s.T <= kStepTokens) {
-    p.step = true;
-    return p;
-  }
-  const int L = sel_lanes(s.N), dg = s.D / s.G;
-  auto blocks = [&](int ch) { return static_cast<int64_t>(s.B) * s.G * ceil_div(dg, ch); };
-  const int wide = 32 / L * kWideGroups, narrow = 32 / L * kTileGroups;
-  p.one_pass = blocks(wide) >= 4 * kSms;
-  p.ch = p.one_pass ? wide : narrow;
+  p.step = s.T <= kStepTokens;
   p.tokens_per_split = s.T;
-  if (!p.one_pass) {
-    const int64_t base = blocks(narrow);
-    const int tiles = static_cast<int>(ceil_div(s.T, kTileTokens));
-    const int64_t want = base <= kSms / 4 ? std::min<int64_t>(kSms / base, tiles / 4) : 1;
-    if (want > 1) {
-      p.tokens_per_split = static_cast<int>(ceil_div(tiles, want)) * kTileTokens;
-      p.splits = static_cast<int>(ceil_div(s.T, p.tokens_per_split));
-      p.state_bytes = align256(static_cast<size_t>(s.B) * p.splits * s.D * s.N * sizeof(float));
-    }
-  }
+  if (p.step) return p;
+  const int64_t warps =
+      static_cast<int64_t>(s.B) * s.G * ceil_div(s.D / s.G, sel_channels(s.N)) * (sdm::kSelThreads / 32);
+  if (warps >= 6 * kSms) return p;
+  const int64_t splits = std::min<int64_t>(ceil_div(32 * kSms, warps), s.T / kSplitTokens);
+  if (splits < 3) return p;
+  const int tile = sdm::kSelTile;
+  p.tokens_per_split = static_cast<int>(ceil_div(ceil_div(s.T, splits), tile) * tile);
+  p.splits = static_cast<int>(ceil_div(s.T, p.tokens_per_split));
+  p.state_bytes = align256(static_cast<size_t>(s.B) * p.splits * s.D * s.N * sizeof(float));
   return p;
 }
 
-template <typename T, int L>
-sdm_status_t launch_scan_lanes(const SelPlan& p, sdm::SelScanArgs a, int B, const float* h0, float* ws,
-                               cudaStream_t st) {
-  if (p.step) {
-    const int64_t channels = static_cast<int64_t>(B) * a.D;
-    sdm::k_selective_scan_step<T, L><<<static_cast<unsigned>(ceil_div(channels * L, 256)), 256, 0, st>>>(a, channels);
-    return launch_status("selective_scan step launch");
-  }
-  if (p.one_pass) {
-    launch_sel<T, L, kSegTokens, 1, kWideGroups, sdm::kSelRun>(a, B, st);
-    return launch_status("selective_scan launch");
-  }
-  if (p.splits > 1) {
-    sdm::SelScanArgs m = a;
-    m.h_in = nullptr;
-    m.sums = ws;
-    launch_sel<T, L, kSegTokens, kTileWarps, kTileGroups, sdm::kSelSums>(m, B, st);
-    const int64_t per_b = static_cast<int64_t>(a.D) * a.N, total = per_b * B;
-    float* H = ws + static_cast<int64_t>(B) * a.splits * per_b;
-    sdm::k_selective_scan_join<<<static_cast<unsigned>(ceil_div(total, 256)), 256, 0, st>>>(ws, H, h0, per_b,
-                                                                                           a.splits, total);
-    a.h_in = H;
-    a.in_splits = 1;
-  }
-  launch_sel<T, L, kSegTokens, kTileWarps, kTileGroups, sdm::kSelRun>(a, B, st);
-  return launch_status("selective_scan launch");
+template <typename T, int kMode>
+void launch_sel(const sdm::SelScanArgs& a, int B, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.tiles_per_group) * a.G, a.splits, B);
+  if (a.N <= 8) sdm::k_selective_scan<T, 8, 1, kMode><<<grid, sdm::kSelThreads, 0, st>>>(a);
+  else if (a.N <= 16) sdm::k_selective_scan<T, 16, 1, kMode><<<grid, sdm::kSelThreads, 0, st>>>(a);
+  else if (a.N <= 32) sdm::k_selective_scan<T, 16, 2, kMode><<<grid, sdm::kSelThreads, 0, st>>>(a);
+  else sdm::k_selective_scan<T, 16, 4, kMode><<<grid, sdm::kSelThreads, 0, st>>>(a);
 }
 
 template <typename T>
-sdm_status_t launch_scan(int L, const SelPlan& p, const sdm::SelScanArgs& a, int B, const float* h0, float* ws,
-                         cudaStream_t st) {
-  switch (L) {
-    case 2: return launch_scan_lanes<T, 2>(p, a, B, h0, ws, st);
-    case 4: return launch_scan_lanes<T, 4>(p, a, B, h0, ws, st);
-    case 8: return launch_scan_lanes<T, 8>(p, a, B, h0, ws, st);
-    default: return launch_scan_lanes<T, 16>(p, a, B, h0, ws, st);
-  }
+void launch_step(const sdm::SelScanArgs& a, int B, cudaStream_t st) {
+  const int64_t channels = static_cast<int64_t>(B) * a.D;
+  auto grid = [&](int lanes) { return static_cast<unsigned>(ceil_div(channels * lanes, 256)); };
+  if (a.N <= 8) sdm::k_selective_scan_step<T, 2><<<grid(2), 256, 0, st>>>(a, channels);
+  else if (a.N <= 16) sdm::k_selective_scan_step<T, 4><<<grid(4), 256, 0, st>>>(a, channels);
+  else if (a.N <= 32) sdm::k_selective_scan_step<T, 8><<<grid(8), 256, 0, st>>>(a, channels);
+  else sdm::k_selective_scan_step<T, 16><<<grid(16), 256, 0, st>>>(a, channels);
 }
 
 }  // namespace
+
+sdm_status_t launch_sel_run(int32_t in_dtype, const sdm::SelScanArgs& a, int B, cudaStream_t st) {
+  if (in_dtype == SDM_BF16) launch_sel<bf16, sdm::kSelRun>(a, B, st);
+  else launch_sel<float, sdm::kSelRun>(a, B, st);
+  return launch_status("selective_scan launch");
+}
+
+sdm_status_t launch_sel_states(int32_t in_dtype, sdm::SelScanArgs a, int B, const float* h0, float* ws,
+                               cudaStream_t st) {
+  a.h_in = nullptr;
+  a.in_splits = 0;
+  a.h_out = nullptr;
+  a.sums = ws;
+  if (in_dtype == SDM_BF16) launch_sel<bf16, sdm::kSelSums>(a, B, st);
+  else launch_sel<float, sdm::kSelSums>(a, B, st);
+  const int64_t per_b = static_cast<int64_t>(a.D) * a.N, total = per_b * B;
+  sdm::k_selective_scan_join<<<static_cast<unsigned>(ceil_div(total, 256)), 256, 0, st>>>(
+      ws, ws + total * a.splits, h0, per_b, a.splits, total);
+  return launch_status("selective_scan state launch");
+}
 
 sdm_status_t check_selscan(const sdm_selscan_shape_t* s) {
   if (s == nullptr) return fail(SDM_ERR_INVALID_ARGUMENT, "shape is NULL");
@@ -128,8 +121,8 @@ sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const
   a.tokens_per_split = s.T;
   a.softplus = s.softplus != 0;
   a.err = err;
-  // Rows read in units of four: address, stride and the group's first channel
-  // (and state) on whole units.
+  // Rows read in units of four: address, stride and each group's first channel
+  // (or state) on whole units.
   const size_t unit = 4 * in_size(s.in_dtype);
   auto whole = [&](const void* p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % unit == 0 && stride % 4 == 0;
@@ -202,14 +195,22 @@ sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x,
   a.h_in = h0;
   a.h_out = hT;
   a.y = y;
-  if (!p.step) {
-    a.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, p.ch));
+  if (p.step) {
+    if (s.in_dtype == SDM_BF16) launch_step<bf16>(a, s.B, st);
+    else launch_step<float>(a, s.B, st);
+    r = launch_status("selective_scan step launch");
+  } else {
+    a.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, sel_channels(s.N)));
     a.splits = p.splits;
     a.tokens_per_split = p.tokens_per_split;
+    if (p.splits > 1) {
+      float* ws = static_cast<float*>(workspace);
+      if ((r = launch_sel_states(s.in_dtype, a, s.B, h0, ws, st)) != SDM_OK) return r;
+      a.h_in = ws + static_cast<int64_t>(s.B) * s.D * s.N * p.splits;
+      a.in_splits = 1;
+    }
+    r = launch_sel_run(s.in_dtype, a, s.B, st);
   }
-  const int L = sel_lanes(s.N);
-  float* ws = static_cast<float*>(workspace);
-  r = s.in_dtype == SDM_BF16 ? launch_scan<bf16>(L, p, a, s.B, h0, ws, st) : launch_scan<float>(L, p, a, s.B, h0, ws, st);
   if (r != SDM_OK) return r;
   return ok();
 }

@@ -20,13 +20,20 @@ struct SelGradPlan {
   size_t total() const { return ckpt + 2 * part_bc + part_A + 2 * part_D; }
 };
 
+// Lanes of a channel in the gradient: four states a lane, two lanes at least.
+int grad_lanes(int32_t N) {
+  int L = 2;
+  while (4 * L < N) L *= 2;
+  return L;
+}
+
 SelGradPlan sel_grad_plan(const sdm_selscan_shape_t& s) {
   SelGradPlan p;
-  p.ch = 32 / sel_lanes(s.N) * kGradGroups;
+  p.ch = 32 / grad_lanes(s.N) * kGradGroups;
   p.tiles = static_cast<int>(ceil_div(s.T, kGradTokens));
   p.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, p.ch));
   const size_t f = sizeof(float);
-  p.ckpt = align256(static_cast<size_t>(s.B) * p.tiles * s.D * s.N * f);
+  p.ckpt = align256(2 * static_cast<size_t>(s.B) * p.tiles * s.D * s.N * f);  // decays, states
   p.part_bc = align256(static_cast<size_t>(p.tiles_per_group) * s.B * s.T * s.G * s.N * f);
   p.part_A = align256(static_cast<size_t>(s.B) * s.D * s.N * f);
   p.part_D = align256(static_cast<size_t>(s.B) * s.D * f);
@@ -36,13 +43,6 @@ SelGradPlan sel_grad_plan(const sdm_selscan_shape_t& s) {
 template <typename T, int L>
 sdm_status_t launch_grad_lanes(const SelGradPlan& p, const sdm::SelGradArgs& a, int B, cudaStream_t st) {
   constexpr int S = kGradSegment<L>, W = kGradTokens / S;
-  // States before the tiles: the forward's segment maps over tiles of the same 64 tokens.
-  constexpr int CS = 16, CWarps = kGradTokens / CS, CGroups = 4;
-  sdm::SelScanArgs f = a.f;
-  f.tiles_per_group = static_cast<int>(ceil_div(f.D / f.G, 32 / L * CGroups));
-  launch_sel<T, L, CS, CWarps, CGroups, sdm::kSelCkpt>(f, B, st);
-  sdm_status_t r;
-  if ((r = launch_status("selective_scan_backward state launch")) != SDM_OK) return r;
   using Tile = sdm::SelGradTile<L, S, W, kGradGroups>;
   constexpr size_t smem = Tile::kSmemFloats * sizeof(float);
   set_smem(reinterpret_cast<const void*>(sdm::k_selective_scan_backward<T, L, S, W, kGradGroups>), smem);
@@ -115,6 +115,7 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
     return ok();
   }
   const SelGradPlan p = sel_grad_plan(s);
+  if (p.tiles > 65535) return fail(SDM_ERR_UNSUPPORTED, "T above 65535 * 64 tokens");
   if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
   if (workspace_bytes < p.total())
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_selective_scan_backward_workspace_bytes");
@@ -122,7 +123,6 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   if ((r = device_info(&dev)) != SDM_OK) return r;
   sdm::SelGradArgs a{};
   a.f = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths, dev->err);
-  a.f.h_in = h0;
   a.f.tiles_per_group = p.tiles_per_group;
   char* ws = static_cast<char*>(workspace);
   auto take = [&](size_t n) {
@@ -130,7 +130,7 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
     ws += n;
     return q;
   };
-  a.f.ckpt = take(p.ckpt);
+  float* ckpt = take(p.ckpt);
   a.part_B = take(p.part_bc);
   a.part_C = take(p.part_bc);
   a.part_A = take(p.part_A);
@@ -142,7 +142,14 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   a.ddt = ddt;
   a.dz = dz;
   a.dstate0 = dh0;
-  const int L = sel_lanes(s.N);
+  // States before the tiles: the forward's maps over splits of one tile each.
+  sdm::SelScanArgs f = a.f;
+  f.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, sel_channels(s.N)));
+  f.splits = p.tiles;
+  f.tokens_per_split = kGradTokens;
+  if ((r = launch_sel_states(s.in_dtype, f, s.B, h0, ckpt, st)) != SDM_OK) return r;
+  a.ckpt = ckpt + static_cast<int64_t>(s.B) * p.tiles * s.D * s.N;
+  const int L = grad_lanes(s.N);
   const bool bf = s.in_dtype == SDM_BF16;
   if ((r = bf ? launch_grad<bf16>(L, p, a, s.B, st) : launch_grad<float>(L, p, a, s.B, st)) != SDM_OK) return r;
   const int64_t n = static_cast<int64_t>(s.B) * s.T * s.G * s.N;
