@@ -1,0 +1,99 @@
+"""Global gradient norm and clipping against 64-bit definitions."""
+
+import math
+
+import pytest
+import torch
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def total(grads):
+    return math.sqrt(sum(float((ref.d(g) ** 2).sum()) for g in grads))
+
+
+def check(sdm, grads, max_norm, outs=None, eps=1e-6):
+    """The norm is exact but for eight squares' fp32 sum (8 roundings, halved) and its own rounding; c adds two, the
+    product one."""
+    n = total(grads)
+    before = [ref.d(g).clone() for g in grads]
+    got = sdm.grad_norm_clip(grads, max_norm, eps=eps, out=outs)
+    assert got.dtype == F32 and got.shape == ()
+    assert abs(float(got) - n) <= 6 * ref.U * n
+    c = min(1.0, max_norm / (n + eps))
+    for b, o in zip(before, grads if outs is None else outs):
+        ref.assert_within(o.reshape(-1), (b * c).reshape(-1), 8 * ref.U * (b * c).abs().reshape(-1), "scaled")
+    return got
+
+
+SIZES = [[1], [3, 5], [2048], [2049, 7, 1, 4096], [100_003, 17, 0, 70_000, 8], [600_000, 1_000_001]]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=str)
+@pytest.mark.parametrize("dtype,out", [(F32, None), (BF16, None), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+def test_values(sdm, sizes, dtype, out, max_norm):
+    g = torch.Generator().manual_seed(len(sizes))
+    grads = [torch.randn(n, generator=g).to(dtype).cuda() for n in sizes]
+    outs = None if out is None else [torch.empty(n, dtype=out, device="cuda") for n in sizes]
+    check(sdm, grads, max_norm, outs)
+
+
+def test_many_tensors(sdm):
+    """More tensors than one launch takes, of mixed types and shapes, views that start anywhere."""
+    g = torch.Generator().manual_seed(0)
+    flat = torch.randn(200_000, generator=g).cuda()
+    grads, at = [], 1
+    for i in range(900):
+        n = (i * 37) % 211
+        grads.append(flat[at:at + n] if i % 3 else torch.randn(max(1, i % 5), 3, generator=g).to(BF16).cuda())
+        at += n
+    check(sdm, grads, 2.0, [torch.empty(t.shape, dtype=F32, device="cuda") for t in grads])
+    check(sdm, grads, 2.0)
+
+
+def test_untouched_where_nothing_is_clipped(sdm):
+    g = torch.randn(5000, generator=torch.Generator().manual_seed(1)).cuda()
+    before = g.clone()
+    sdm.grad_norm_clip([g], 1e6)
+    assert torch.equal(g, before)
+    norm = sdm.grad_norm_clip([g], float("inf"))
+    assert torch.equal(g, before) and abs(float(norm) - total([before])) <= 6 * ref.U * total([before])
+    out = torch.empty_like(g)
+    sdm.grad_norm_clip([g], float("inf"), out=[out])
+    assert torch.equal(out, before)
+
+
+@pytest.mark.parametrize("scale", [1e25, 1e-25, 1e-38])
+def test_squares_beyond_fp32(sdm, scale):
+    g = (torch.randn(3000, generator=torch.Generator().manual_seed(2)).double() * scale).float().cuda()
+    n = total([g])
+    got = sdm.grad_norm_clip([g], float("inf"))
+    assert abs(float(got) - n) <= 6 * ref.U * n + 2.0 ** -149
+
+
+def test_zero_and_empty(sdm):
+    z = torch.zeros(70, device="cuda")
+    assert float(sdm.grad_norm_clip([z, torch.empty(0, device="cuda")], 1.0)) == 0.0 and not z.any()
+    assert float(sdm.grad_norm_clip([torch.empty(0, device="cuda")], 1.0)) == 0.0
+
+
+def test_not_finite(sdm):
+    """A norm that is not finite does what the formula says: 0 for infinity (0 * inf is not a number), NaN for NaN."""
+    g = torch.ones(100, device="cuda")
+    g[3] = float("inf")
+    out = torch.empty_like(g)
+    assert math.isinf(float(sdm.grad_norm_clip([g], 1.0, out=[out])))
+    assert math.isnan(float(out[3])) and float(out[0]) == 0.0
+    g[3] = float("nan")
+    assert math.isnan(float(sdm.grad_norm_clip([g], 1.0, out=[out]))) and bool(torch.isnan(out).all())
+
+
+def test_same_bits_every_time(sdm):
+    g = [torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda() for n in (1_000_003, 77, 250_000)]
+    first = sdm.grad_norm_clip(g, float("inf"))
+    for _ in range(5):
+        assert torch.equal(sdm.grad_norm_clip(g, float("inf")), first)
