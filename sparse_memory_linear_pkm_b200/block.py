@@ -11,6 +11,7 @@ and batch rows.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 
 import torch
@@ -28,12 +29,20 @@ def _code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _at(t: torch.Tensor | None, what: str, dev: torch.device, shape=None, dtype=None, contiguous=True):
+def _device(t: torch.Tensor) -> int:
+    """Index of the CUDA device that a call's first tensor lives on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return dev
+
+
+def _at(t: torch.Tensor | None, what: str, dev: int, shape=None, dtype=None, contiguous=True):
     """Address of a tensor (None for None) after checking where it lives and, when given, what it is."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, not on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on cuda:{dev}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -43,26 +52,20 @@ def _at(t: torch.Tensor | None, what: str, dev: torch.device, shape=None, dtype=
     return t.data_ptr()
 
 
-def _device(t: torch.Tensor) -> torch.device:
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    return t.device
-
-
-def _call(dev: torch.device, fn, *args) -> None:
-    """Enqueues a library call on the current stream of dev."""
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(dev: int, fn, *args) -> None:
+    """Enqueues a library call on the current stream of dev, whichever device is current."""
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         native.check(status)
 
 
-def _workspace(nbytes: int, dev: torch.device):
+def _workspace(nbytes: int, like: torch.Tensor):
     """Scratch of one call, from the allocator of the current stream (None for no bytes)."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _needed(lib, nbytes: int, nonempty: bool) -> int:
@@ -75,18 +78,19 @@ def _needed(lib, nbytes: int, nonempty: bool) -> int:
 
 def _token_stride(t: torch.Tensor, inner: int, what: str) -> int:
     """Elements from token to token of a [B, T, ...] tensor whose axes behind the second hold `inner` elements in order."""
-    if not t.is_contiguous():
-        B, T = t.shape[:2]
-        run = 1
-        for n, s in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-            if n > 1 and s != run:
-                raise ValueError(f"{what} must be contiguous behind its token axis")
-            run *= n
-        step = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else inner)
-        if step < inner or (B > 1 and t.stride(0) != T * step):
-            raise ValueError(f"{what} must be evenly spaced over tokens and batch rows")
-        return step
-    return inner
+    if t.is_contiguous():
+        return inner
+    shape, stride = t.shape, t.stride()
+    run = 1
+    for i in range(len(shape) - 1, 1, -1):
+        if shape[i] > 1 and stride[i] != run:
+            raise ValueError(f"{what} must be contiguous behind its token axis")
+        run *= shape[i]
+    B, T = shape[0], shape[1]
+    step = stride[1] if T > 1 else (stride[0] if B > 1 else inner)
+    if step < inner or (B > 1 and stride[0] != T * step):
+        raise ValueError(f"{what} must be evenly spaced over tokens and batch rows")
+    return step
 
 
 # -------------------------------------------------------------------- norm --
@@ -112,19 +116,20 @@ def rmsnorm_residual(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | 
     if residual is not None:
         res_code = _code(residual, "residual")
         if h is None:
-            h = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            h = torch.empty_like(residual)
     elif h is not None:
         raise ValueError("h needs a residual: without one it is x")
     scales = None
     if y_code == native.FP8_B16:
-        y = torch.empty(n * d + n * d // 16, dtype=torch.uint8, device=dev)
-        at_y, at_scales = y.data_ptr(), y.data_ptr() + n * d
+        y = x.new_empty(n * d + n * d // 16, dtype=torch.uint8)
+        at_y = y.data_ptr()
+        at_scales = at_y + n * d
     elif y_code == native.FP8_ROW:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+        scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
         at_y, at_scales = y.data_ptr(), scales.data_ptr()
     else:
-        y = torch.empty(x.shape, dtype=torch.bfloat16 if y_code == native.BF16 else torch.float32, device=dev)
+        y = x.new_empty(x.shape, dtype=torch.bfloat16 if y_code == native.BF16 else torch.float32)
         at_y, at_scales = y.data_ptr(), None
     _call(dev, native.load().sdm_rmsnorm_residual, _at(x, "x", dev), x_code,
           _at(residual, "residual", dev, x.shape), res_code, _at(w, "w", dev, (d,)), _code(w, "w"), n, d, eps,
@@ -136,7 +141,7 @@ def dequantize_fp8blk(buf: torch.Tensor, shape, dtype: torch.dtype = torch.float
     """The values of a block-scaled fp8 buffer (quantize_fp8blk, rmsnorm_residual
     with out="fp8blk") as a tensor of the given shape and type."""
     dev = _device(buf)
-    y = torch.empty(shape, dtype=dtype, device=dev)
+    y = buf.new_empty(shape, dtype=dtype)
     n = y.numel()
     if n % 16 or buf.numel() != n + n // 16:
         raise ValueError(f"a buffer of {n} values holds {n + n // 16} bytes, n a multiple of 16; got {buf.numel()}")
@@ -149,7 +154,7 @@ def dequantize_fp8row(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dt
     """codes [..., d] (float8_e4m3fn) times scales [...] (fp32), as values of the given type."""
     dev = _device(codes)
     d = codes.shape[-1]
-    y = torch.empty(codes.shape, dtype=dtype, device=dev)
+    y = codes.new_empty(codes.shape, dtype=dtype)
     _call(dev, native.load().sdm_dequantize_fp8row, _at(codes, "codes", dev, dtype=torch.float8_e4m3fn),
           _at(scales, "scales", dev, codes.shape[:-1], torch.float32), codes.numel() // d if d else 0, d, y.data_ptr(),
           _code(y, "dtype"))
@@ -165,9 +170,9 @@ def rmsnorm_residual_backward(h: torch.Tensor, w: torch.Tensor, dy: torch.Tensor
     n = h.numel() // d if d else 0
     lib = native.load()
     ws_bytes = _needed(lib, lib.sdm_rmsnorm_residual_backward_workspace_bytes(n, d), n > 0)
-    ws = _workspace(ws_bytes, dev)
-    dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
-    dw = torch.empty(d, dtype=torch.float32, device=dev)
+    ws = _workspace(ws_bytes, h)
+    dx = torch.empty_like(h)
+    dw = h.new_empty(d, dtype=torch.float32)
     _call(dev, lib.sdm_rmsnorm_residual_backward, _at(h, "h", dev), _code(h, "h"), _at(w, "w", dev, (d,)),
           _code(w, "w"), _at(dy, "dy", dev, h.shape), _code(dy, "dy"), _at(dh, "dh", dev, h.shape, h.dtype), n, d, eps,
           dx.data_ptr(), dw.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes)
@@ -197,8 +202,7 @@ def short_conv(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     dev = _device(x)
     B, T, D, K = _conv_sizes(x, w, bias)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if lengths is None else torch.zeros(
-            x.shape, dtype=x.dtype, device=dev)
+        y = x.new_empty(x.shape) if lengths is None else x.new_zeros(x.shape)
     _call(dev, native.load().sdm_short_conv, _at(x, "x", dev, contiguous=False), _token_stride(x, D, "x"),
           _code(x, "x"), _at(w, "w", dev), _at(bias, "bias", dev, (D,)), _code(w, "w"), B, T, D, K, int(silu),
           _at(state, "state", dev, (B, K - 1, D), x.dtype), _at(lengths, "lengths", dev, (B,), torch.int32),
@@ -216,13 +220,13 @@ def short_conv_backward(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, bias
     B, T, D, K = _conv_sizes(x, w, bias)
     lib = native.load()
     ws_bytes = _needed(lib, lib.sdm_short_conv_backward_workspace_bytes(B, T, D, K), B * T * D > 0)
-    ws = _workspace(ws_bytes, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = torch.empty((D, K), dtype=torch.float32, device=dev)
-    dbias = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
+    ws = _workspace(ws_bytes, x)
+    dx = x.new_empty(x.shape)
+    dw = x.new_empty((D, K), dtype=torch.float32)
+    dbias = x.new_empty(D, dtype=torch.float32) if bias is not None else None
     dstate0 = None
     if state0 is not None or dstate is not None:
-        dstate0 = torch.empty((B, K - 1, D), dtype=x.dtype, device=dev)
+        dstate0 = x.new_empty((B, K - 1, D))
     _call(dev, lib.sdm_short_conv_backward, _at(x, "x", dev, contiguous=False), _token_stride(x, D, "x"),
           _code(x, "x"), _at(w, "w", dev), _at(bias, "bias", dev, (D,)), _code(w, "w"), B, T, D, K, int(silu),
           _at(state0, "state0", dev, (B, K - 1, D), x.dtype), _at(lengths, "lengths", dev, (B,), torch.int32),
@@ -269,10 +273,9 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     lib = native.load()
     ref = ctypes.byref(shape)
     ws_bytes = lib.sdm_selective_scan_workspace_bytes(ref)
-    ws = _workspace(ws_bytes, dev)
+    ws = _workspace(ws_bytes, x)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if lengths is None else torch.zeros(
-            x.shape, dtype=x.dtype, device=dev)
+        y = x.new_empty(x.shape) if lengths is None else x.new_zeros(x.shape)
     at_state = _at(state, "state", dev, (shape.B, shape.D, shape.N), torch.float32)
     _call(dev, lib.sdm_selective_scan, ref, *args, at_state, at_state, _at(y, "y", dev, x.shape, x.dtype),
           None if ws is None else ws.data_ptr(), ws_bytes)
@@ -292,14 +295,14 @@ def selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, 
     lib = native.load()
     ref = ctypes.byref(shape)
     ws_bytes = _needed(lib, lib.sdm_selective_scan_backward_workspace_bytes(ref), x.numel() > 0)
-    ws = _workspace(ws_bytes, dev)
-    like = lambda t: torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
+    ws = _workspace(ws_bytes, x)
+    like = lambda t: t.new_empty(t.shape)  # noqa: E731
     states = (shape.B, shape.D, shape.N)
     out = {"dx": like(x), "ddt": like(x), "dA": like(A), "dB": like(B), "dC": like(B),
            "dD": None if D is None else like(D), "dz": None if z is None else like(x),
            "ddt_bias": None if dt_bias is None else like(dt_bias), "dstate0": None}
     if state0 is not None or dstate is not None:
-        out["dstate0"] = torch.empty(states, dtype=torch.float32, device=dev)
+        out["dstate0"] = A.new_empty(states)
     at = {k: None if v is None else v.data_ptr() for k, v in out.items()}
     _call(dev, lib.sdm_selective_scan_backward, ref, *args, _at(state0, "state0", dev, states, torch.float32),
           _at(dy, "dy", dev, x.shape, x.dtype), _at(dstate, "dstate", dev, states, torch.float32), at["dx"], at["ddt"],
@@ -323,22 +326,35 @@ def grad_norm_clip(grads, max_norm: float, eps: float = 1e-6, out=None) -> torch
     if not grads:
         raise ValueError("no gradients")
     dev = _device(grads[0])
-    flat = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if g.device != dev or o.device != dev:
-            raise ValueError(f"gradient {i} or its output is not on {dev}")
-        if not g.is_contiguous() or not o.is_contiguous():
-            raise ValueError(f"gradient {i} and its output must be contiguous")
-        n = g.numel()
-        if o is not g and o.numel() != n:
-            raise ValueError(f"output {i} has {o.numel()} values, its gradient {n}")
-        flat += (g.data_ptr(), o.data_ptr(), n, _code(g, f"gradient {i}") | _code(o, f"output {i}") << 32)
-    if out is None and max_norm == float("inf"):
-        flat[1::4] = [0] * len(grads)
-    table = struct.pack(f"={len(flat)}q", *flat)  # an array of sdm_grad_tensor_t
+    # A list has hundreds of tensors: each is asked as little as possible, and which one is wrong only then.
+    at, codes, sizes = _flat(grads, dev, "gradient")
+    if out is None:
+        out_at, out_codes = ([0] * len(at) if max_norm == math.inf else at), codes
+    else:
+        out_at, out_codes, out_sizes = _flat(outs, dev, "output")
+        if out_sizes != sizes:
+            i = next(i for i, (a, b) in enumerate(zip(out_sizes, sizes)) if a != b)
+            raise ValueError(f"output {i} has {out_sizes[i]} values, its gradient {sizes[i]}")
+    table = [0] * (4 * len(at))  # an array of sdm_grad_tensor_t
+    table[::4], table[1::4], table[2::4] = at, out_at, sizes
+    table[3::4] = [a | b << 32 for a, b in zip(codes, out_codes)]
     lib = native.load()
-    ws_bytes = lib.sdm_grad_norm_clip_workspace_bytes(len(grads))
-    ws = _workspace(ws_bytes, dev)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    _call(dev, lib.sdm_grad_norm_clip, table, len(grads), max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws_bytes)
+    ws_bytes = lib.sdm_grad_norm_clip_workspace_bytes(len(at))
+    ws = _workspace(ws_bytes, grads[0])
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    _call(dev, lib.sdm_grad_norm_clip, struct.pack(f"={len(table)}q", *table), len(at), max_norm, eps, norm.data_ptr(),
+          ws.data_ptr(), ws_bytes)
     return norm
+
+
+def _flat(tensors, dev: int, what: str):
+    """Addresses, type codes and sizes of contiguous tensors on dev."""
+    try:
+        codes = [_CODE[t.dtype] for t in tensors]
+    except KeyError:
+        i = next(i for i, t in enumerate(tensors) if t.dtype not in _CODE)
+        raise TypeError(f"{what} {i} must be float32 or bfloat16, got {tensors[i].dtype}") from None
+    if not all([t.is_contiguous() and t.get_device() == dev for t in tensors]):
+        i = next(i for i, t in enumerate(tensors) if not (t.is_contiguous() and t.get_device() == dev))
+        raise ValueError(f"{what} {i} must be contiguous and on cuda:{dev}")
+    return [t.data_ptr() for t in tensors], codes, [t.numel() for t in tensors]

@@ -4,9 +4,12 @@
 //
 // with the K - 1 inputs before the first token in `state` (zeros without one),
 // which ends as the last K - 1 inputs. Bound by memory: 2 K operations and a
-// sigmoid per value moved twice. A thread owns neighbouring channels (one
-// 8- or 16-byte unit) over a run of tokens, so that each input is loaded once per run
-// plus the K - 1 before it, and neighbouring threads read neighbouring units.
+// sigmoid per value moved twice. A thread owns neighbouring channels over a run
+// of tokens, so that each input is loaded once per run plus the K - 1 before it,
+// and neighbouring threads read neighbouring units; the loads of a few tokens go
+// out together one such step before they are used (all of a run's loads at once
+// took the registers of the threads that should have hidden them: 215 us instead
+// of @@CONV@@ for a padded batch of 6 x 4099 x 4096 in bf16).
 #pragma once
 
 #include "sdm_device.cuh"
@@ -25,6 +28,7 @@ struct ConvArgs {
   void* y;             // [B, T, D]
   int64_t x_stride;
   int T, D, K, units;  // units: threads along the channels of one token
+  int run;             // tokens of a thread, a multiple of kConvAhead
   unsigned per_seq;    // threads with work per sequence: units x runs of tokens
   int w_bf16, silu;
   unsigned* err;
@@ -50,90 +54,151 @@ __device__ __forceinline__ int clamp_length(const int32_t* lengths, int b, int T
   return n;
 }
 
-// Weight k of the KT-tap window for channel c: the K given taps are the last K
-// of KT, the ones before them are 0.
-template <int KT>
-__device__ __forceinline__ float conv_weight(const void* w, int bf, int c, int k, int K) {
-  const int i = k - (KT - K);
-  if (i < 0) return 0.f;
-  const int64_t at = static_cast<int64_t>(c) * K + i;
-  return bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at]) : static_cast<const float*>(w)[at];
+// The KT-tap window of V channels from c0, as channel pairs, of which n exist:
+// the K given taps are the last K of KT, the ones before them are 0.
+template <int KT, int V>
+__device__ __forceinline__ void conv_weights(const void* w, int bf, int c0, int n, int K, float2 (*out)[V / 2]) {
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = 0.f;
+      const int tap = k - (KT - K);
+      if (tap >= 0 && i < n) {
+        const int64_t at = static_cast<int64_t>(c0 + i) * K + tap;
+        v[i] = bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at]) : static_cast<const float*>(w)[at];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) out[k][i] = make_float2(v[2 * i], v[2 * i + 1]);
+  }
 }
-__device__ __forceinline__ float conv_param(const void* p, int bf, int c) {
-  return bf ? to_f32<bf16>(static_cast<const bf16*>(p)[c]) : static_cast<const float*>(p)[c];
+template <int V>
+__device__ __forceinline__ void conv_bias(const void* p, int bf, int c0, int n, float2* out) {
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = 0.f;
+    if (p != nullptr && i < n) v[i] = bf ? to_f32<bf16>(static_cast<const bf16*>(p)[c0 + i]) : static_cast<const float*>(p)[c0 + i];
+  }
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) out[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
 
-// V channels a thread (V > 1: whole aligned units), L tokens a run. The thread
-// of a sequence's first run also moves the state: it alone reads the old one,
-// and the new one comes from x and the old one, so both may be one buffer.
-template <typename T, int KT, int V, int L>
+// A thread's V channels of one row: whole aligned units (kVec), or the n that
+// exist one at a time.
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void conv_load(RawUnit<T, V>& r, const T* p, int n) {
+  if (kVec) r.load(p);
+  else r.load_some(p, n);
+}
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void conv_store(T* p, int n, const float2* o) {
+  if (kVec) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[2 * i] = o[i].x, v[2 * i + 1] = o[i].y;
+    store_unit<T, V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if (2 * i < n) p[2 * i] = from_f32<T>(o[i].x);
+      if (2 * i + 1 < n) p[2 * i + 1] = from_f32<T>(o[i].y);
+    }
+  }
+}
+
+constexpr int kConvV = 4;      // channels of a forward thread
+constexpr int kConvAhead = 4;  // tokens loaded together, one such run before they are used
+static_assert(kConvMaxK - 1 <= 2 * kConvAhead, "runs are at least two of these, so only the first reaches the state");
+
+// A thread walks one run of tokens of kConvV channels with the last KT - 1
+// inputs in registers. The thread of a sequence's first run also moves the
+// state: it alone reads the old one, and the new one comes from x and the old
+// one, so both may be one buffer.
+template <typename T, int KT, bool kVec>
 __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
-  static_assert(L >= KT - 1, "only the first run reaches into the state");
+  constexpr int V = kConvV, P = V / 2;
   const unsigned id = blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= a.per_seq) return;
   const int run = static_cast<int>(id / static_cast<unsigned>(a.units));
   const int unit = static_cast<int>(id) - run * a.units, b = blockIdx.y;
-  const int c0 = unit * V, t0 = run * L;
-  const int len = clamp_length(a.lengths, b, a.T, a.err);
-  if (t0 >= len && run != 0) return;
+  const int c0 = unit * V, n = a.D - c0, t0 = run * a.run;
   const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride + c0;
   const int hist = a.K - 1;
   T* state = a.state == nullptr ? nullptr : static_cast<T*>(a.state) + static_cast<int64_t>(b) * hist * a.D + c0;
 
-  float win[KT - 1 + L][V];  // inputs t0 - (KT - 1) .. t0 + L - 1
+  float2 w[KT][P], bias[P];
+  conv_weights<KT, V>(a.w, a.w_bf16, c0, n, a.K, w);
+  conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
+  const int len = clamp_length(a.lengths, b, a.T, a.err);
+  const int t1 = min(len, t0 + a.run);
+  if (t0 >= len && run != 0) return;
+
+  RawUnit<T, V> old[KT - 1], next[kConvAhead];
 #pragma unroll
-  for (int i = 0; i < KT - 1 + L; ++i) {
-    const int t = t0 + i - (KT - 1);
-    if (t >= 0 && t < len) {
-      load_unit<T, V>(x + t * a.x_stride, win[i]);
-    } else if (t < 0 && t >= -hist && state != nullptr) {
-      load_unit<T, V>(state + static_cast<int64_t>(hist + t) * a.D, win[i]);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) win[i][v] = 0.f;
-    }
+  for (int i = 0; i < KT - 1; ++i) {
+    const int t = t0 - (KT - 1) + i;
+    old[i].zero();
+    if (t >= 0) conv_load<T, V, kVec>(old[i], x + t * a.x_stride, n);
+    else if (t >= -hist && state != nullptr) conv_load<T, V, kVec>(old[i], state + static_cast<int64_t>(hist + t) * a.D, n);
   }
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i) {
+      next[i].zero();
+      if (t + i < t1) conv_load<T, V, kVec>(next[i], x + (t + i) * a.x_stride, n);
+    }
+  };
+  fetch(t0);
   if (run == 0 && state != nullptr) {
-    // Row j of the new state is input len - hist + j: of the old state where
-    // that is negative (then it is in the window), else of x.
-    float row[KT - 1][V];
+    // Row j of the new state is input len - hist + j, of the old state where
+    // that is negative: row len + j of it. All are read before any is written.
+    RawUnit<T, V> row[KT - 1];
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) {
       const int t = len - hist + j;
-      if (j < hist) {
-        if (t >= 0) {
-          load_unit<T, V>(x + t * a.x_stride, row[j]);
-        } else {
-          load_unit<T, V>(state + static_cast<int64_t>(hist + t) * a.D, row[j]);
-        }
-      }
+      if (j < hist) conv_load<T, V, kVec>(row[j], t >= 0 ? x + t * a.x_stride : state + static_cast<int64_t>(hist + t) * a.D, n);
     }
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j)
-      if (j < hist) store_unit<T, V>(state + static_cast<int64_t>(j) * a.D, row[j]);
-  }
-  if (t0 >= len) return;
-  float w[KT][V], bias[V];
+      if (j < hist) {
+        float2 v[P];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = a.bias == nullptr ? 0.f : conv_param(a.bias, a.w_bf16, c0 + v);
-#pragma unroll
-    for (int k = 0; k < KT; ++k) w[k][v] = conv_weight<KT>(a.w, a.w_bf16, c0 + v, k, a.K);
-  }
-  T* y = static_cast<T*>(a.y) + (static_cast<int64_t>(b) * a.T + t0) * a.D + c0;
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    if (t0 + i < len) {
-      float o[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float u = bias[v];
-#pragma unroll
-        for (int k = 0; k < KT; ++k) u = fmaf(w[k][v], win[i + k][v], u);
-        o[v] = a.silu ? silu_fast(u) : u;
+        for (int p = 0; p < P; ++p) v[p] = row[j].pair(p);
+        conv_store<T, V, kVec>(state + static_cast<int64_t>(j) * a.D, n, v);
       }
-      store_unit<T, V>(y + static_cast<int64_t>(i) * a.D, o);
+  }
+  float2 win[KT - 1 + kConvAhead][P];
+#pragma unroll
+  for (int i = 0; i < KT - 1; ++i)
+#pragma unroll
+    for (int p = 0; p < P; ++p) win[i][p] = old[i].pair(p);
+  T* y = static_cast<T*>(a.y) + (static_cast<int64_t>(b) * a.T + t0) * a.D + c0;
+  for (int t = t0; t < t1; t += kConvAhead) {
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p) win[KT - 1 + i][p] = next[i].pair(p);
+    fetch(t + kConvAhead);
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i) {
+      float2 o[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        o[p] = bias[p];
+#pragma unroll
+        for (int k = 0; k < KT; ++k) o[p] = fma2(w[k][p], win[i + k][p], o[p]);
+        if (a.silu) o[p] = make_float2(silu_fast(o[p].x), silu_fast(o[p].y));
+      }
+      if (t + i < t1) conv_store<T, V, kVec>(y + static_cast<int64_t>(i) * a.D, n, o);
     }
+    y += static_cast<int64_t>(kConvAhead) * a.D;
+#pragma unroll
+    for (int i = 0; i < KT - 1; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p) win[i][p] = win[kConvAhead + i][p];
   }
 }
 
@@ -157,116 +222,116 @@ struct ConvGradArgs {
   unsigned* err;
 };
 
-constexpr int kConvGradLanes = 32, kConvGradRows = 8;  // units x segments of a block
+constexpr int kConvGradV = 2;                           // channels of a gradient thread
+constexpr int kConvGradLanes = 32, kConvGradRows = 8;   // units x segments of a block
 
 // With du = dy act'(u): dx_t = sum_k w[k] du_{t+K-1-k}, dw[k] = sum_t du_t
 // x_{t-K+1+k}, db = sum_t du_t. A thread walks one segment of tokens with the
-// last KT inputs and KT du in registers; the block's segments of a channel are
-// added in shared memory in a fixed order, and the blocks' sums by k_sum_slots.
-// The extended sequence has K - 1 rows before token 0 (dstate0) and the
-// derivative of the final state reaches the last K - 1 inputs.
-template <typename T, int KT, int V>
+// last inputs and du in registers; the block's segments of a channel are added
+// in shared memory in a fixed order, and the blocks' sums by k_short_conv_sums.
+// Two channels a thread keep its registers few enough for the loads of enough
+// threads to be on their way. The extended sequence has K - 1 rows before token
+// 0 (dstate0), and the derivative of the final state reaches the last K - 1
+// inputs.
+template <typename T, int KT, bool kVec>
 __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_backward(const ConvGradArgs a) {
-  __shared__ float sums[kConvGradRows][KT + 1][kConvGradLanes * V];
+  constexpr int V = kConvGradV, kAhead = kConvAhead;
+  __shared__ float2 sums[kConvGradRows][KT + 1][kConvGradLanes];
   const int lane = threadIdx.x, row = threadIdx.y;
-  const int unit = blockIdx.x * kConvGradLanes + lane, c0 = unit * V;
+  const int unit = blockIdx.x * kConvGradLanes + lane, c0 = unit * V, n = a.D - c0;
   const int64_t s = static_cast<int64_t>(blockIdx.y) * kConvGradRows + row;
-  float dw[KT][V], db[V];
+  float2 dw[KT], db = both(0.f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    db[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KT; ++k) dw[k][v] = 0.f;
-  }
+  for (int k = 0; k < KT; ++k) dw[k] = both(0.f);
   if (unit < a.units && s < static_cast<int64_t>(a.B) * a.segs) {
     const int b = static_cast<int>(s / a.segs), t0 = static_cast<int>(s % a.segs) * a.seg;
     const int t1 = min(a.T, t0 + a.seg);
-    const int len = clamp_length(a.lengths, b, a.T, a.err);
     const int hist = a.K - 1;
-    float w[KT][V], bias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      bias[v] = a.bias == nullptr ? 0.f : conv_param(a.bias, a.w_bf16, c0 + v);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) w[k][v] = conv_weight<KT>(a.w, a.w_bf16, c0 + v, k, a.K);
-    }
+    float2 w[KT][1], bias[1];
+    conv_weights<KT, V>(a.w, a.w_bf16, c0, n, a.K, w);
+    conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
+    const int len = clamp_length(a.lengths, b, a.T, a.err);
     const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride + c0;
     const T* dy = static_cast<const T*>(a.dy) + static_cast<int64_t>(b) * a.T * a.D + c0;
     T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(b) * a.T * a.D + c0;
     const int64_t sb = static_cast<int64_t>(b) * hist * a.D + c0;
-    float xw[KT][V], duw[KT][V];  // inputs t - KT + 1 .. t, du of the same tokens
+    // Slot j of xw and du is token t - (KT - 1) + j, t the first of a run of
+    // kAhead; du before the segment is not needed (another segment's outputs).
+    float2 xw[KT - 1 + kAhead], du[KT - 1 + kAhead];
+    RawUnit<T, V> rx[kAhead], rd[kAhead], r;
+    const int t_load = min(len, t1 + KT - 1);
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const int t = t0 - KT + k;  // shifted by one before the first step
+      for (int i = 0; i < kAhead; ++i) {
+        rx[i].zero();
+        rd[i].zero();
+        if (t + i < t_load) {
+          conv_load<T, V, kVec>(rx[i], x + (t + i) * a.x_stride, n);
+          conv_load<T, V, kVec>(rd[i], dy + static_cast<int64_t>(t + i) * a.D, n);
+        }
+      }
+    };
+    fetch(t0);
 #pragma unroll
-      for (int v = 0; v < V; ++v) xw[k][v] = 0.f, duw[k][v] = 0.f;
-      if (t >= 0 && t < len) load_unit<T, V>(x + t * a.x_stride, xw[k]);
+    for (int j = 0; j < KT - 1; ++j) {
+      const int t = t0 - (KT - 1) + j;
+      du[j] = both(0.f);
+      r.zero();
+      if (t >= 0 && t < len) conv_load<T, V, kVec>(r, x + t * a.x_stride, n);
       else if (t < 0 && t >= -hist && a.state0 != nullptr)
-        load_unit<T, V>(static_cast<const T*>(a.state0) + sb + static_cast<int64_t>(hist + t) * a.D, xw[k]);
+        conv_load<T, V, kVec>(r, static_cast<const T*>(a.state0) + sb + static_cast<int64_t>(hist + t) * a.D, n);
+      xw[j] = r.pair(0);
     }
     // Token t's du completes dx of token t - (KT - 1). The first segment also
     // finishes the K - 1 rows before token 0.
-#pragma unroll 4
-    for (int t = t0; t < t1 + KT - 1; ++t) {
-      float xn[V], dn[V];
+    for (int t = t0; t < t1 + KT - 1; t += kAhead) {
+      float2 dn[kAhead];
 #pragma unroll
-      for (int v = 0; v < V; ++v) xn[v] = 0.f, dn[v] = 0.f;
-      if (t < len) {
-        load_unit<T, V>(x + t * a.x_stride, xn);
-        load_unit<T, V>(dy + static_cast<int64_t>(t) * a.D, dn);
+      for (int i = 0; i < kAhead; ++i) {
+        xw[KT - 1 + i] = rx[i].pair(0);
+        dn[i] = rd[i].pair(0);
+      }
+      fetch(t + kAhead);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        float2 g = dn[i];
+        if (a.silu && t + i < len) {
+          float2 u = bias[0];
+#pragma unroll
+          for (int k = 0; k < KT; ++k) u = fma2(w[k][0], xw[i + k], u);
+          g = mul2(g, make_float2(silu_grad_fast(u.x), silu_grad_fast(u.y)));
+        }
+        du[KT - 1 + i] = g;
+        if (t + i < t1) {
+          db.x += g.x;
+          db.y += g.y;
+#pragma unroll
+          for (int k = 0; k < KT; ++k) dw[k] = fma2(g, xw[i + k], dw[k]);
+        }
+        const int to = t + i - (KT - 1);  // its window of du is complete now
+        if (to < t1 && (to >= t0 || (t0 == 0 && to >= -hist))) {
+          float2 o = both(0.f);
+#pragma unroll
+          for (int k = 0; k < KT; ++k) o = fma2(w[k][0], du[i + KT - 1 - k], o);
+          // Input `to` is row to - (len - hist) of the final state.
+          const int j = to - (len - hist);
+          if (a.dstate != nullptr && j >= 0 && j < hist) {
+            conv_load<T, V, kVec>(r, static_cast<const T*>(a.dstate) + sb + static_cast<int64_t>(j) * a.D, n);
+            o.x += r.pair(0).x;
+            o.y += r.pair(0).y;
+          }
+          if (to >= 0) conv_store<T, V, kVec>(dx + static_cast<int64_t>(to) * a.D, n, &o);
+          else if (a.dstate0 != nullptr)
+            conv_store<T, V, kVec>(static_cast<T*>(a.dstate0) + sb + static_cast<int64_t>(hist + to) * a.D, n, &o);
+        }
       }
 #pragma unroll
-      for (int k = 0; k + 1 < KT; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) xw[k][v] = xw[k + 1][v], duw[k][v] = duw[k + 1][v];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        xw[KT - 1][v] = xn[v];
-        float du = dn[v];
-        if (a.silu && t < len) {
-          float u = bias[v];
-#pragma unroll
-          for (int k = 0; k < KT; ++k) u = fmaf(w[k][v], xw[k][v], u);
-          du *= silu_grad_fast(u);
-        }
-        duw[KT - 1][v] = du;
-        if (t < t1) {
-          db[v] += du;
-#pragma unroll
-          for (int k = 0; k < KT; ++k) dw[k][v] = fmaf(du, xw[k][v], dw[k][v]);
-        }
-      }
-      const int to = t - (KT - 1);  // its window of du is complete now
-      if (to >= t0 || (t0 == 0 && to >= -hist)) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          o[v] = 0.f;
-#pragma unroll
-          for (int k = 0; k < KT; ++k) o[v] = fmaf(w[k][v], duw[KT - 1 - k][v], o[v]);
-        }
-        // Input `to` is row to - (len - hist) of the final state.
-        const int j = to - (len - hist);
-        if (a.dstate != nullptr && j >= 0 && j < hist) {
-          float ds[V];
-          load_unit<T, V>(static_cast<const T*>(a.dstate) + sb + static_cast<int64_t>(j) * a.D, ds);
-#pragma unroll
-          for (int v = 0; v < V; ++v) o[v] += ds[v];
-        }
-        if (to >= 0) {
-          store_unit<T, V>(dx + static_cast<int64_t>(to) * a.D, o);
-        } else if (a.dstate0 != nullptr) {
-          store_unit<T, V>(static_cast<T*>(a.dstate0) + sb + static_cast<int64_t>(hist + to) * a.D, o);
-        }
-      }
+      for (int j = 0; j < KT - 1; ++j) xw[j] = xw[kAhead + j], du[j] = du[kAhead + j];
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int k = 0; k < KT; ++k) sums[row][k][lane * V + v] = dw[k][v];
-    sums[row][KT][lane * V + v] = db[v];
-  }
+  for (int k = 0; k < KT; ++k) sums[row][k][lane] = dw[k];
+  sums[row][KT][lane] = db;
   __syncthreads();
   const int tid = row * kConvGradLanes + lane;
   for (int i = tid; i < (a.K + 1) * kConvGradLanes * V; i += kConvGradLanes * kConvGradRows) {
@@ -275,7 +340,10 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_b
     if (c < a.D) {
       float v = 0.f;
 #pragma unroll
-      for (int r = 0; r < kConvGradRows; ++r) v += sums[r][k < a.K ? k + KT - a.K : KT][cc];
+      for (int q = 0; q < kConvGradRows; ++q) {
+        const float2 f = sums[q][k < a.K ? k + KT - a.K : KT][cc / 2];
+        v += cc % 2 == 0 ? f.x : f.y;
+      }
       a.part[(static_cast<int64_t>(blockIdx.y) * a.D + c) * (a.K + 1) + k] = v;
     }
   }

@@ -12,7 +12,6 @@ using sdm::bf16;
 
 namespace {
 
-constexpr int kUnit = 4;      // channels of a thread where rows are whole aligned units
 constexpr int kGradSeg = 64;  // tokens of a gradient thread
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -32,9 +31,9 @@ sdm_status_t check_conv(int32_t B, int32_t T, int32_t D, int32_t K, int64_t x_st
   return SDM_OK;
 }
 
-// Whether rows of D values at this address and stride are whole units of kUnit.
-bool whole_units(const void* x, int64_t x_stride, int32_t D, int32_t dtype) {
-  return D % kUnit == 0 && x_stride % kUnit == 0 && reinterpret_cast<uintptr_t>(x) % (kUnit * in_size(dtype)) == 0;
+// Whether rows of D values at this address and stride are whole units of V.
+bool whole_units(const void* x, int64_t x_stride, int32_t D, int32_t dtype, int V) {
+  return D % V == 0 && x_stride % V == 0 && reinterpret_cast<uintptr_t>(x) % (V * in_size(dtype)) == 0;
 }
 
 // Whether two arrays of these sizes share a byte.
@@ -43,21 +42,19 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return a < b + m && b < a + n;
 }
 
-template <typename T, int KT, int L>
-void launch_conv_run(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
+template <typename T, int KT>
+void launch_conv_taps(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(ceil_div(a.per_seq, 256)), B);
-  if (vec) sdm::k_short_conv<T, KT, kUnit, L><<<grid, 256, 0, st>>>(a);
-  else sdm::k_short_conv<T, KT, 1, L><<<grid, 256, 0, st>>>(a);
+  if (vec) sdm::k_short_conv<T, KT, true><<<grid, 256, 0, st>>>(a);
+  else sdm::k_short_conv<T, KT, false><<<grid, 256, 0, st>>>(a);
 }
 
-// Runs of 16 tokens move each input 1 + (K - 1) / 16 times; a call whose
-// sequences fit in one run of 8 (single tokens above all) takes that instead.
-template <typename T, int KT>
-void launch_conv_taps(bool vec, sdm::ConvArgs a, int B, cudaStream_t st) {
-  const int L = a.T <= 8 ? 8 : 16;
-  a.per_seq = static_cast<unsigned>(a.units * ceil_div(a.T, L));
-  if (L == 8) launch_conv_run<T, KT, 8>(vec, a, B, st);
-  else launch_conv_run<T, KT, 16>(vec, a, B, st);
+// Tokens of a thread: up to 64 (the K - 1 inputs before a run are read twice),
+// fewer while the threads would not fill the device's 148 SMs with 1024 each.
+int conv_run(int B, int T, int units) {
+  int run = 64;
+  while (run > 2 * sdm::kConvAhead && static_cast<int64_t>(B) * units * ceil_div(T, run) < 148 * 1024) run /= 2;
+  return run;
 }
 
 template <typename T>
@@ -69,8 +66,8 @@ void launch_conv(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
 template <typename T, int KT>
 void launch_conv_grad_taps(bool vec, const sdm::ConvGradArgs& a, dim3 grid, cudaStream_t st) {
   const dim3 block(sdm::kConvGradLanes, sdm::kConvGradRows);
-  if (vec) sdm::k_short_conv_backward<T, KT, kUnit><<<grid, block, 0, st>>>(a);
-  else sdm::k_short_conv_backward<T, KT, 1><<<grid, block, 0, st>>>(a);
+  if (vec) sdm::k_short_conv_backward<T, KT, true><<<grid, block, 0, st>>>(a);
+  else sdm::k_short_conv_backward<T, KT, false><<<grid, block, 0, st>>>(a);
 }
 
 struct ConvGradPlan {
@@ -113,9 +110,10 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
     return fail(SDM_ERR_INVALID_ARGUMENT, "y overlaps x (threads read neighbours' inputs)");
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  const bool vec = whole_units(x, stride, D, in_dtype);
-  sdm::ConvArgs a{x, w, bias, state, lengths, y, stride, T, D, K, vec ? D / kUnit : D, 0, w_dtype == SDM_BF16,
-                  silu != 0, dev->err};
+  const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvV);
+  const int units = static_cast<int>(ceil_div(D, sdm::kConvV)), run = conv_run(B, T, units);
+  const sdm::ConvArgs a{x, w, bias, state, lengths, y, stride, T, D, K, units, run,
+                        static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16, silu != 0, dev->err};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (in_dtype == SDM_BF16) launch_conv<bf16>(vec, a, B, st);
   else launch_conv<float>(vec, a, B, st);
@@ -172,10 +170,10 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   if (p.slots > 65535) return fail(SDM_ERR_UNSUPPORTED, "B * T above 65535 * 512 tokens");
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  const bool vec = whole_units(x, stride, D, in_dtype);
+  const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvGradV);
   float* part = static_cast<float*>(workspace);
   const sdm::ConvGradArgs a{x, w, bias, state0, dy, dstate, lengths, dx, dstate0, part, stride, B, T, D, K,
-                            vec ? D / kUnit : D, p.segs, kGradSeg, w_dtype == SDM_BF16, silu != 0, dev->err};
+                            static_cast<int>(ceil_div(D, sdm::kConvGradV)), p.segs, kGradSeg, w_dtype == SDM_BF16, silu != 0, dev->err};
   const dim3 grid(static_cast<unsigned>(ceil_div(a.units, sdm::kConvGradLanes)), static_cast<unsigned>(p.slots));
   if (in_dtype == SDM_BF16) {
     if (K <= 4) launch_conv_grad_taps<bf16, 4>(vec, a, grid, st);

@@ -79,4 +79,63 @@ __device__ __forceinline__ void store8(T* p, const float* v) {
   }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
+      " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 low2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 high2(float4 v) { return make_float2(v.z, v.w); }
+
+// V (two or four) consecutive values as they are in memory: what is loaded long
+// before it is used, so that nothing waits for the load until then.
+template <typename T, int V>
+struct RawUnit {
+  static constexpr int kWords = V * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+    } else if constexpr (kWords == 2) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x; w[1] = q.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  // The first n values, one at a time (zeros behind them): rows that are not whole units.
+  __device__ __forceinline__ void load_some(const T* p, int n) {
+    uint32_t v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = 0u;
+      if (i < n) v[i] = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(p)[i] : reinterpret_cast<const uint16_t*>(p)[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? v[i % V] : v[2 * i % V] | v[(2 * i + 1) % V] << 16;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float2 pair(int i) const {  // values 2 i and 2 i + 1
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+};
+
 }  // namespace sdm
