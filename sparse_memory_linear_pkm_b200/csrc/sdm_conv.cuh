@@ -12,6 +12,8 @@
 // of @@CONV@@ for a padded batch of 6 x 4099 x 4096 in bf16).
 #pragma once
 
+#include <type_traits>
+
 #include "sdm_device.cuh"
 #include "sdm_vec.cuh"
 
@@ -33,14 +35,6 @@ struct ConvArgs {
   int w_bf16, silu;
   unsigned* err;
 };
-
-__device__ __forceinline__ float sigmoid_fast(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
-// u sigmoid(u); below -87 exp(-u) leaves fp32's range and the product is 0.
-__device__ __forceinline__ float silu_fast(float u) { return u < -87.0f ? 0.0f : u * sigmoid_fast(u); }
-__device__ __forceinline__ float silu_grad_fast(float u) {
-  const float g = sigmoid_fast(u);
-  return u < -87.0f ? 0.0f : g * (1.0f + u * (1.0f - g));
-}
 
 // A sequence's length from the caller's array: clamped to [0, T], with the
 // error word set where it was outside.
@@ -144,14 +138,22 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
     if (t >= 0) conv_load<T, V, kVec>(old[i], x + t * a.x_stride, n);
     else if (t >= -hist && state != nullptr) conv_load<T, V, kVec>(old[i], state + static_cast<int64_t>(hist + t) * a.D, n);
   }
-  auto fetch = [&](int t) {
+  const T* ahead = x + t0 * a.x_stride;  // of the tokens to be loaded next, from `left` before the run's end
+  int left = t1 - t0;
+  auto fetch = [&]() {
+    if (left >= kConvAhead) {
 #pragma unroll
-    for (int i = 0; i < kConvAhead; ++i) {
-      next[i].zero();
-      if (t + i < t1) conv_load<T, V, kVec>(next[i], x + (t + i) * a.x_stride, n);
+      for (int i = 0; i < kConvAhead; ++i, ahead += a.x_stride) conv_load<T, V, kVec>(next[i], ahead, n);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kConvAhead; ++i, ahead += a.x_stride) {
+        next[i].zero();
+        if (i < left) conv_load<T, V, kVec>(next[i], ahead, n);
+      }
     }
+    left -= kConvAhead;
   };
-  fetch(t0);
+  fetch();
   if (run == 0 && state != nullptr) {
     // Row j of the new state is input len - hist + j, of the old state where
     // that is negative: row len + j of it. All are read before any is written.
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
     for (int i = 0; i < kConvAhead; ++i)
 #pragma unroll
       for (int p = 0; p < P; ++p) win[KT - 1 + i][p] = next[i].pair(p);
-    fetch(t + kConvAhead);
+    fetch();
 #pragma unroll
     for (int i = 0; i < kConvAhead; ++i) {
       float2 o[P];
@@ -190,11 +192,11 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
         o[p] = bias[p];
 #pragma unroll
         for (int k = 0; k < KT; ++k) o[p] = fma2(w[k][p], win[i + k][p], o[p]);
-        if (a.silu) o[p] = make_float2(silu_fast(o[p].x), silu_fast(o[p].y));
+        if (a.silu) o[p] = silu2(o[p]);
       }
-      if (t + i < t1) conv_store<T, V, kVec>(y + static_cast<int64_t>(i) * a.D, n, o);
+      if (t + i < t1) conv_store<T, V, kVec>(y, n, o);
+      y += a.D;
     }
-    y += static_cast<int64_t>(kConvAhead) * a.D;
 #pragma unroll
     for (int i = 0; i < KT - 1; ++i)
 #pragma unroll
@@ -259,19 +261,30 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_b
     // kAhead; du before the segment is not needed (another segment's outputs).
     float2 xw[KT - 1 + kAhead], du[KT - 1 + kAhead];
     RawUnit<T, V> rx[kAhead], rd[kAhead], r;
-    const int t_load = min(len, t1 + KT - 1);
-    auto fetch = [&](int t) {
+    const T* x_next = x + t0 * a.x_stride;  // of the tokens to be loaded next, from `left` before the last one needed
+    const T* dy_next = dy + static_cast<int64_t>(t0) * a.D;
+    int left = min(len, t1 + KT - 1) - t0;
+    auto fetch = [&]() {
+      if (left >= kAhead) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        rx[i].zero();
-        rd[i].zero();
-        if (t + i < t_load) {
-          conv_load<T, V, kVec>(rx[i], x + (t + i) * a.x_stride, n);
-          conv_load<T, V, kVec>(rd[i], dy + static_cast<int64_t>(t + i) * a.D, n);
+        for (int i = 0; i < kAhead; ++i, x_next += a.x_stride, dy_next += a.D) {
+          conv_load<T, V, kVec>(rx[i], x_next, n);
+          conv_load<T, V, kVec>(rd[i], dy_next, n);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i, x_next += a.x_stride, dy_next += a.D) {
+          rx[i].zero();
+          rd[i].zero();
+          if (i < left) {
+            conv_load<T, V, kVec>(rx[i], x_next, n);
+            conv_load<T, V, kVec>(rd[i], dy_next, n);
+          }
         }
       }
+      left -= kAhead;
     };
-    fetch(t0);
+    fetch();
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) {
       const int t = t0 - (KT - 1) + j;
@@ -283,50 +296,59 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_b
       xw[j] = r.pair(0);
     }
     // Token t's du completes dx of token t - (KT - 1). The first segment also
-    // finishes the K - 1 rows before token 0.
-    for (int t = t0; t < t1 + KT - 1; t += kAhead) {
+    // finishes the K - 1 rows before token 0. Inside the segment (kIn) every
+    // token of a step counts and every output is an ordinary row.
+    const int last = a.dstate == nullptr ? t1 : min(t1, len - hist);  // dx rows that the final state does not reach
+    T* out = dx + static_cast<int64_t>(t0 - (KT - 1)) * a.D;          // row `to` of the next output
+    auto step = [&](int t, auto in) {
+      constexpr bool kIn = decltype(in)::value;
       float2 dn[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         xw[KT - 1 + i] = rx[i].pair(0);
         dn[i] = rd[i].pair(0);
       }
-      fetch(t + kAhead);
+      fetch();
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         float2 g = dn[i];
-        if (a.silu && t + i < len) {
+        if (a.silu && (kIn || t + i < len)) {
           float2 u = bias[0];
 #pragma unroll
           for (int k = 0; k < KT; ++k) u = fma2(w[k][0], xw[i + k], u);
-          g = mul2(g, make_float2(silu_grad_fast(u.x), silu_grad_fast(u.y)));
+          g = mul2(g, silu_grad2(u));
         }
         du[KT - 1 + i] = g;
-        if (t + i < t1) {
-          db.x += g.x;
-          db.y += g.y;
+        if (kIn || t + i < t1) {
+          db = add2(db, g);
 #pragma unroll
           for (int k = 0; k < KT; ++k) dw[k] = fma2(g, xw[i + k], dw[k]);
         }
         const int to = t + i - (KT - 1);  // its window of du is complete now
-        if (to < t1 && (to >= t0 || (t0 == 0 && to >= -hist))) {
+        if (kIn || (to < t1 && (to >= t0 || (t0 == 0 && to >= -hist)))) {
           float2 o = both(0.f);
 #pragma unroll
           for (int k = 0; k < KT; ++k) o = fma2(w[k][0], du[i + KT - 1 - k], o);
-          // Input `to` is row to - (len - hist) of the final state.
-          const int j = to - (len - hist);
-          if (a.dstate != nullptr && j >= 0 && j < hist) {
-            conv_load<T, V, kVec>(r, static_cast<const T*>(a.dstate) + sb + static_cast<int64_t>(j) * a.D, n);
-            o.x += r.pair(0).x;
-            o.y += r.pair(0).y;
+          if (!kIn && a.dstate != nullptr) {
+            // Input `to` is row to - (len - hist) of the final state.
+            const int j = to - (len - hist);
+            if (j >= 0 && j < hist) {
+              conv_load<T, V, kVec>(r, static_cast<const T*>(a.dstate) + sb + static_cast<int64_t>(j) * a.D, n);
+              o = add2(o, r.pair(0));
+            }
           }
-          if (to >= 0) conv_store<T, V, kVec>(dx + static_cast<int64_t>(to) * a.D, n, &o);
+          if (kIn || to >= 0) conv_store<T, V, kVec>(out, n, &o);
           else if (a.dstate0 != nullptr)
             conv_store<T, V, kVec>(static_cast<T*>(a.dstate0) + sb + static_cast<int64_t>(hist + to) * a.D, n, &o);
         }
+        out += a.D;
       }
 #pragma unroll
       for (int j = 0; j < KT - 1; ++j) xw[j] = xw[kAhead + j], du[j] = du[kAhead + j];
+    };
+    for (int t = t0; t < t1 + KT - 1; t += kAhead) {
+      if (t - (KT - 1) >= t0 && t + kAhead <= min(t1, len) && t + kAhead - (KT - 1) <= last) step(t, std::true_type());
+      else step(t, std::false_type());
     }
   }
 #pragma unroll

@@ -31,7 +31,6 @@
 
 namespace sdm {
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct SelScanArgs {
@@ -60,12 +59,6 @@ struct SelScanArgs {
 };
 
 enum SelMode { kSelRun = 0, kSelSums = 1 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // softplus of two values: max(u, 0) + log(1 + e), e = exp(-|u|) in (0, 1], with
 // log(1 + e) = e q(e). q is the polynomial of degree 8 with the least relative
@@ -289,10 +282,12 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan(const SelScanArg
         if (a.softplus) p = softplus2(p);
         d[i] = t1 + i < t_end ? p.x : 0.f;  // a step of 0 leaves the state as it is
         d[i + 1] = t1 + i + 1 < t_end ? p.y : 0.f;
-#pragma unroll
-        for (int j = i; j < i + 2; ++j) {
-          x[j] = t1 + j < t_end ? rx[j].get() : 0.f;
-          gate[j] = gated ? silu_fast(rz[j].get()) : 1.0f;
+        x[i] = t1 + i < t_end ? rx[i].get() : 0.f;
+        x[i + 1] = t1 + i + 1 < t_end ? rx[i + 1].get() : 0.f;
+        if (gated) {
+          const float2 g = silu2(make_float2(rz[i].get(), rz[i + 1].get()));
+          gate[i] = g.x;
+          gate[i + 1] = g.y;
         }
       }
       ahead(t1 + kSelAhead);
@@ -316,7 +311,8 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan(const SelScanArg
           float o = (y[0].x + y[0].y) + (y[1].x + y[1].y);
 #pragma unroll
           for (int q = L / 2; q > 0; q >>= 1) o += __shfl_xor_sync(0xffffffffu, o, q);
-          o = fmaf(skip, x[i], o) * gate[i];
+          o = fmaf(skip, x[i], o);
+          if (gated) o *= gate[i];
           if (writes && t1 + i < t_end) gy[i * static_cast<int64_t>(a.D)] = from_f32<T>(o);
         } else {
           total += d[i];
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(256) k_selective_scan_step(const SelScanArgs a
     for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
     if (on && l == 0) {
       y = fmaf(skip, x, y);
-      if (a.z != nullptr) y *= silu_fast(z);
+      if (a.z != nullptr) y *= silu2(both(z)).x;
       static_cast<T*>(a.y)[tok * a.D + c] = from_f32<T>(y);
     }
   }

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(32 * W * CG) k_selective_scan_backward(const S
         if (t0 + tt < len && c0 + my_c + v < c_end) d = a.softplus ? softplus2(both(pre[u][v])).x : pre[u][v];
         if (i < TT * UR) {
           s_dx[tt * CH + my_c + v] = make_float2(d, d * x[u][v]);
-          s_e[tt * CH + my_c + v] = gz != nullptr ? dy[u][v] * silu_fast(z[u][v]) : dy[u][v];
+          s_e[tt * CH + my_c + v] = gz != nullptr ? dy[u][v] * silu2(both(z[u][v])).x : dy[u][v];
         }
       }
     }
@@ -404,11 +404,11 @@ __global__ void __launch_bounds__(32 * W * CG) k_selective_scan_backward(const S
           if (t < len && v < n) {
             o_x[v] = fmaf(s_dx[at].x, p, skip[v] * w);
             float dd = fmaf(xv, p, s_r[at]);
-            if (a.softplus) dd *= sigmoid_fast(fmaxf(pre[uu][v], -87.0f));
+            if (a.softplus) dd *= sigmoid2(both(pre[uu][v])).x;
             o_t[v] = dd;
             dbias[v] += dd;
             dD[v] = fmaf(w, xv, dD[v]);
-            if (gz != nullptr) o_z[v] = dy[uu][v] * fmaf(skip[v], xv, s_y[at]) * silu_grad_fast(z[uu][v]);
+            if (gz != nullptr) o_z[v] = dy[uu][v] * fmaf(skip[v], xv, s_y[at]) * silu_grad2(both(z[uu][v])).x;
           }
         }
         const int64_t at = out0 + static_cast<int64_t>(t) * a.D + c0 + my_c;

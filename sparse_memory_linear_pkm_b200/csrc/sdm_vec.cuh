@@ -96,9 +96,45 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 low2(float4 v) { return make_float2(v.x, v.y); }
 __device__ __forceinline__ float2 high2(float4 v) { return make_float2(v.z, v.w); }
+
+// 2^x and 1 / x, off by at most two units in the last place; results below
+// fp32's normal range are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// sigmoid(u) = 1 / (1 + exp(-u)) of two values. Where exp(-u) leaves fp32's
+// range the result is 0, and so are SiLU and its derivative.
+__device__ __forceinline__ float2 sigmoid2(float2 u) {
+  const float2 t = mul2(u, both(-kLog2e));
+  const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.0f));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
+__device__ __forceinline__ float2 silu2(float2 u) { return mul2(u, sigmoid2(u)); }
+// (u sigmoid(u))' = g + g u (1 - g), g = sigmoid(u).
+__device__ __forceinline__ float2 silu_grad2(float2 u) {
+  const float2 g = sigmoid2(u);
+  return fma2(g, fma2(make_float2(-g.x, -g.y), u, u), g);
+}
 
 // V (two or four) consecutive values as they are in memory: what is loaded long
 // before it is used, so that nothing waits for the load until then.
