@@ -32,7 +32,7 @@ struct ConvArgs {
   int T, D, K, units;  // units: threads along the channels of one token
   int run;             // tokens of a thread, a multiple of kConvAhead
   unsigned per_seq;    // threads with work per sequence: units x runs of tokens
-  int w_bf16, silu;
+  int w_bf16, w_whole, silu;
   unsigned* err;
 };
 
@@ -49,24 +49,32 @@ __device__ __forceinline__ int clamp_length(const int32_t* lengths, int b, int T
 }
 
 // The KT-tap window of V channels from c0, as channel pairs, of which n exist:
-// the K given taps are the last K of KT, the ones before them are 0.
+// the K given taps are the last K of KT, the ones before them are 0. `whole`:
+// K = KT = 4 and a channel's taps are one aligned unit.
 template <int KT, int V>
-__device__ __forceinline__ void conv_weights(const void* w, int bf, int c0, int n, int K, float2 (*out)[V / 2]) {
+__device__ __forceinline__ void conv_weights(const void* w, int bf, bool whole, int c0, int n, int K,
+                                             float2 (*out)[V / 2]) {
+  float v[V][KT];
 #pragma unroll
-  for (int k = 0; k < KT; ++k) {
-    float v[V];
+  for (int i = 0; i < V; ++i) {
+    const int64_t at = static_cast<int64_t>(c0 + i) * K;
+    if (KT == 4 && whole && i < n) {
+      if (bf) load_unit<bf16, 4>(static_cast<const bf16*>(w) + at, v[i]);
+      else load_unit<float, 4>(static_cast<const float*>(w) + at, v[i]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = 0.f;
-      const int tap = k - (KT - K);
-      if (tap >= 0 && i < n) {
-        const int64_t at = static_cast<int64_t>(c0 + i) * K + tap;
-        v[i] = bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at]) : static_cast<const float*>(w)[at];
+      for (int k = 0; k < KT; ++k) {
+        const int tap = k - (KT - K);
+        v[i][k] = 0.f;
+        if (tap >= 0 && i < n)
+          v[i][k] = bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at + tap]) : static_cast<const float*>(w)[at + tap];
       }
     }
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) out[k][i] = make_float2(v[2 * i], v[2 * i + 1]);
   }
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) out[k][i] = make_float2(v[2 * i][k], v[2 * i + 1][k]);
 }
 template <int V>
 __device__ __forceinline__ void conv_bias(const void* p, int bf, int c0, int n, float2* out) {
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
   T* state = a.state == nullptr ? nullptr : static_cast<T*>(a.state) + static_cast<int64_t>(b) * hist * a.D + c0;
 
   float2 w[KT][P], bias[P];
-  conv_weights<KT, V>(a.w, a.w_bf16, c0, n, a.K, w);
+  conv_weights<KT, V>(a.w, a.w_bf16, a.w_whole, c0, n, a.K, w);
   conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
   const int len = clamp_length(a.lengths, b, a.T, a.err);
   const int t1 = min(len, t0 + a.run);
@@ -220,7 +228,7 @@ struct ConvGradArgs {
   int64_t x_stride;
   int B, T, D, K, units;
   int segs, seg;          // segments of `seg` tokens per sequence
-  int w_bf16, silu;
+  int w_bf16, w_whole, silu;
   unsigned* err;
 };
 
@@ -236,7 +244,8 @@ constexpr int kConvGradLanes = 32, kConvGradRows = 8;   // units x segments of a
 // 0 (dstate0), and the derivative of the final state reaches the last K - 1
 // inputs.
 template <typename T, int KT, bool kVec>
-__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_backward(const ConvGradArgs a) {
+__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, KT == 4 ? 3 : 1)
+    k_short_conv_backward(const ConvGradArgs a) {
   constexpr int V = kConvGradV, kAhead = kConvAhead;
   __shared__ float2 sums[kConvGradRows][KT + 1][kConvGradLanes];
   const int lane = threadIdx.x, row = threadIdx.y;
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows) k_short_conv_b
     const int t1 = min(a.T, t0 + a.seg);
     const int hist = a.K - 1;
     float2 w[KT][1], bias[1];
-    conv_weights<KT, V>(a.w, a.w_bf16, c0, n, a.K, w);
+    conv_weights<KT, V>(a.w, a.w_bf16, a.w_whole, c0, n, a.K, w);
     conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
     const int len = clamp_length(a.lengths, b, a.T, a.err);
     const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride + c0;

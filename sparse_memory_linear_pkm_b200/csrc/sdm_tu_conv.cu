@@ -36,6 +36,11 @@ bool whole_units(const void* x, int64_t x_stride, int32_t D, int32_t dtype, int 
   return D % V == 0 && x_stride % V == 0 && reinterpret_cast<uintptr_t>(x) % (V * in_size(dtype)) == 0;
 }
 
+// Whether a channel's taps are one aligned unit of four.
+bool whole_taps(const void* w, int32_t dtype, int32_t K) {
+  return K == 4 && reinterpret_cast<uintptr_t>(w) % (4 * in_size(dtype)) == 0;
+}
+
 // Whether two arrays of these sizes share a byte.
 bool overlap(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
@@ -113,7 +118,7 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
   const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvV);
   const int units = static_cast<int>(ceil_div(D, sdm::kConvV)), run = conv_run(B, T, units);
   const sdm::ConvArgs a{x, w, bias, state, lengths, y, stride, T, D, K, units, run,
-                        static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16, silu != 0, dev->err};
+                        static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (in_dtype == SDM_BF16) launch_conv<bf16>(vec, a, B, st);
   else launch_conv<float>(vec, a, B, st);
@@ -173,7 +178,7 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvGradV);
   float* part = static_cast<float*>(workspace);
   const sdm::ConvGradArgs a{x, w, bias, state0, dy, dstate, lengths, dx, dstate0, part, stride, B, T, D, K,
-                            static_cast<int>(ceil_div(D, sdm::kConvGradV)), p.segs, kGradSeg, w_dtype == SDM_BF16, silu != 0, dev->err};
+                            static_cast<int>(ceil_div(D, sdm::kConvGradV)), p.segs, kGradSeg, w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const dim3 grid(static_cast<unsigned>(ceil_div(a.units, sdm::kConvGradLanes)), static_cast<unsigned>(p.slots));
   if (in_dtype == SDM_BF16) {
     if (K <= 4) launch_conv_grad_taps<bf16, 4>(vec, a, grid, st);
