@@ -49,14 +49,15 @@ __device__ __forceinline__ int norm_col(int j, int i, int t, int tpr) {
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void norm_load(const T* row, int j, int t, int tpr, int d, float* v) {
+__device__ __forceinline__ void norm_load(const T* row, int j, int t, int tpr, int d, float2* pairs) {
+  float v[8];
   if (kVec) {
     if (norm_col<true>(j, 0, t, tpr) < d) {
       load8<T>(row + norm_col<true>(j, 0, t, tpr), v);
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -64,9 +65,14 @@ __device__ __forceinline__ void norm_load(const T* row, int j, int t, int tpr, i
       v[i] = c < d ? to_f32<T>(row[c]) : 0.f;
     }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pairs[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
 template <typename T, bool kVec>
-__device__ __forceinline__ void norm_store(T* row, int j, int t, int tpr, int d, const float* v) {
+__device__ __forceinline__ void norm_store(T* row, int j, int t, int tpr, int d, const float2* pairs) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[2 * i] = pairs[i].x, v[2 * i + 1] = pairs[i].y;
   if (kVec) {
     if (norm_col<true>(j, 0, t, tpr) < d) store8<T>(row + norm_col<true>(j, 0, t, tpr), v);
   } else {
@@ -79,27 +85,43 @@ __device__ __forceinline__ void norm_store(T* row, int j, int t, int tpr, int d,
 }
 
 struct OpSum {
-  template <typename T>
-  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+  __device__ __forceinline__ float over(float v, int o) const { return v + __shfl_xor_sync(0xffffffffu, v, o); }
 };
-struct OpMax {
-  __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+struct OpSum2 {
+  __device__ __forceinline__ float2 operator()(float2 a, float2 b) const { return add2(a, b); }
+  __device__ __forceinline__ float2 over(float2 v, int o) const {
+    return add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  }
+};
+// A 64-bit sum and an fp32 maximum.
+struct SumMax {
+  double sum;
+  float max;
+};
+struct OpSumMax {
+  __device__ __forceinline__ SumMax operator()(SumMax a, SumMax b) const {
+    return {a.sum + b.sum, fmaxf(a.max, b.max)};
+  }
+  __device__ __forceinline__ SumMax over(SumMax v, int o) const {
+    return (*this)(v, {__shfl_xor_sync(0xffffffffu, v.sum, o), __shfl_xor_sync(0xffffffffu, v.max, o)});
+  }
 };
 
 // Reduction over the tpr threads of a row, the result in all of them: within
-// groups of tpr <= 32 lanes, or (kBlock) over the whole block through `buf`
-// (one value per warp), in a fixed order. Every thread of the block calls it.
+// groups of tpr <= 32 lanes, or (kBlock) over the whole block through `buf` (one
+// value per warp), in a fixed order. Every thread of the block calls it. There
+// is one barrier a call: consecutive calls alternate between two buffers.
 template <bool kBlock, typename T, typename Op>
 __device__ __forceinline__ T row_reduce(T v, int tpr, T* buf, Op op) {
   const int top = kBlock ? 16 : tpr / 2;
-  for (int o = top; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = top; o > 0; o >>= 1) v = op.over(v, o);
   if (kBlock) {
     const int warps = blockDim.x / kWarp;
     if (lane_id() == 0) buf[threadIdx.x / kWarp] = v;
     __syncthreads();
     v = buf[0];
     for (int i = 1; i < warps; ++i) v = op(v, buf[i]);
-    __syncthreads();
   }
   return v;
 }
@@ -121,24 +143,26 @@ __device__ __forceinline__ float to_f32_odd(double v) {
   return static_cast<double>(f) == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// Whether the fp32 u, off by at most 8 units in the last place, may round to
-// another E4M3 value than the number it stands for: its distance from a border
-// (the middle between two E4M3 values; below 2^-6 they are 2^-9 apart).
-__device__ __forceinline__ bool e4m3_near_border(float u) {
-  const float a = fabsf(u);
-  if (a >= 0.015625f) {
-    const int low = static_cast<int>(__float_as_uint(a) & 0xFFFFFu) - 0x80000;
-    return low > -16 && low < 16;
-  }
-  const float q = a * 512.0f;
-  return fabsf(q - floorf(q) - 0.5f) < 1e-5f;
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ uint2 e4m3x8(const float2* u) {
+  return make_uint2(e4m3x2(u[0]) | e4m3x2(u[1]) << 16, e4m3x2(u[2]) | e4m3x2(u[3]) << 16);
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
-}
-__device__ __forceinline__ uint2 e4m3x8(const float* u) {
-  return make_uint2(e4m3x2(u[0], u[1]) | e4m3x2(u[2], u[3]) << 16, e4m3x2(u[4], u[5]) | e4m3x2(u[6], u[7]) << 16);
+// Codes of eight fp32 values whose errors are some 2^-23 relative; *sure tells
+// whether they are the codes of the numbers the values stand for: both ends of
+// 1 +- 2^-20 around each value round to one code.
+__device__ __forceinline__ uint2 e4m3x8_sure(const float2* u, bool* sure) {
+  float2 lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = mul2(u[i], both(1.0f - 0x1p-20f));
+    hi[i] = mul2(u[i], both(1.0f + 0x1p-20f));
+  }
+  const uint2 a = e4m3x8(lo), b = e4m3x8(hi);
+  *sure = a.x == b.x && a.y == b.y;
+  return b;
 }
 
 // Block exponent of the 8-bit format for a block maximum f * 2^k, f in [0.5, 1).
@@ -146,110 +170,156 @@ __device__ __forceinline__ int fp8blk_exponent(bool above, int k) {
   return min(127, max(-127, (k - 9) + (above ? 1 : 0)));
 }
 
-// One thread's half of a 16-value block (the other half is lane ^ 1's): codes
-// and the block's exponent of the real h s w.
-__device__ __forceinline__ uint2 norm_fp8blk(const float* h, const float* w, double s, bool live, int* e_out) {
-  const float sf = static_cast<float>(s);
-  float u[8], mx = 0.f;
+// The real h w k of eight values, rounded to odd.
+__device__ __forceinline__ void real_products(const float2* h, const float2* w, double k, float2* u) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    u[i] = h[i] * w[i] * sf;
-    mx = fmaxf(mx, fabsf(u[i]));
+  for (int i = 0; i < 4; ++i)
+    u[i] = make_float2(to_f32_odd(static_cast<double>(h[i].x) * static_cast<double>(w[i].x) * k),
+                       to_f32_odd(static_cast<double>(h[i].y) * static_cast<double>(w[i].y) * k));
+}
+// max |h w| of eight values in 64 bits (not a number does not count).
+__device__ __forceinline__ double real_max(const float2* h, const float2* w) {
+  double m = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m = fmax(m, fabs(static_cast<double>(h[i].x) * static_cast<double>(w[i].x)));
+    m = fmax(m, fabs(static_cast<double>(h[i].y) * static_cast<double>(w[i].y)));
+  }
+  return m;
+}
+
+// One thread's half of a 16-value block (the other half is lane ^ 1's): codes
+// and the block's exponent of the real h w s.
+__device__ __forceinline__ uint2 norm_fp8blk(const float2* h, const float2* w, double s, bool live, int* e_out) {
+  const float2 sf = both(static_cast<float>(s));
+  float2 u[4];
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    u[i] = mul2(mul2(h[i], w[i]), sf);
+    mx = fmaxf(mx, fmaxf(fabsf(u[i].x), fabsf(u[i].y)));
   }
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  int e = 0;
-  bool near = !(mx > 1e-30f && mx < 3e38f);  // the ends of fp32's range, and zeros, go the 64-bit way
-  if (!near) {
-    int k;
-    const float f = frexpf(mx, &k);
-    e = fp8blk_exponent(f > 0.90625f, k);
-    near = fabsf(f - 0.90625f) < 1e-6f;
-    const float inv = pow2f(-e);
+  // mx = f 2^k, f in [0.5, 1); the ends of fp32's range, and zeros, go the 64-bit way.
+  bool sure = mx > 1e-30f && mx < 3e38f;
+  const uint32_t bits = __float_as_uint(mx);
+  const float f = __uint_as_float((bits & 0x007FFFFFu) | 0x3F000000u);
+  int e = sure ? fp8blk_exponent(f > 0.90625f, static_cast<int>(bits >> 23) - 126) : 0;
+  sure = sure && fabsf(f - 0.90625f) > 1e-6f;
+  const float2 inv = both(pow2f(-e));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[i] *= inv;
-      near |= e4m3_near_border(u[i]);
-    }
-  }
-  near = live && near;
-  near |= __shfl_xor_sync(0xffffffffu, static_cast<int>(near), 1) != 0;
-  if (__any_sync(0xffffffffu, near)) {
-    double m = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmax(m, fabs(static_cast<double>(h[i]) * static_cast<double>(w[i]) * s));
+  for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], inv);
+  bool codes_sure;
+  uint2 codes = e4m3x8_sure(u, &codes_sure);
+  const int unsure = live && !(sure && codes_sure);
+  if (__any_sync(0xffffffffu, unsure)) {
+    const bool redo = unsure | __shfl_xor_sync(0xffffffffu, unsure, 1);
+    double m = real_max(h, w) * s;
     m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if (near) {
+    if (redo) {
       int k = 0;
-      const double f = m > 0.0 && m < 1e300 ? frexp(m, &k) : 0.0;
-      e = f > 0.0 ? fp8blk_exponent(f > 0.90625, k) : (m > 0.0 ? 127 : 0);
-      const double inv = scalbn(1.0, -e);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        u[i] = to_f32_odd(static_cast<double>(h[i]) * static_cast<double>(w[i]) * s * inv);
+      const double f64 = m > 0.0 && m < 1e300 ? frexp(m, &k) : 0.0;
+      e = f64 > 0.0 ? fp8blk_exponent(f64 > 0.90625, k) : (m > 0.0 ? 127 : 0);
+      real_products(h, w, s * scalbn(1.0, -e), u);
+      codes = e4m3x8(u);
     }
   }
   *e_out = e;
-  return e4m3x8(u);
+  return codes;
+}
+
+// The scale of a row whose largest real |y| is m: m / 448 rounded to fp32 once,
+// at least the least normal fp32; 1 for a row of zeros.
+__device__ __forceinline__ float fp8row_scale(double m) {
+  if (!(m > 0.0)) return 1.0f;
+  const double t = m * (1.0 / 448.0);  // off by less than 2^-51 relative
+  float c = static_cast<float>(t * (1.0 - 0x1p-50));
+  if (c != static_cast<float>(t * (1.0 + 0x1p-50))) c = static_cast<float>(m / 448.0);
+  return fmaxf(c, 1.17549435e-38f);
+}
+
+// s / c for an fp32 c: two Newton steps from its fp32 reciprocal.
+__device__ __forceinline__ double quotient64(double s, float c) {
+  const double d = static_cast<double>(c);
+  if (!(c > 1e-30f && c < 1e30f)) return s / d;
+  double r = static_cast<double>(rcp(c));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = fma(r, fma(-d, r, 1.0), r);
+  return s * r;
 }
 
 template <typename Tx, typename Tr, int kOut, bool kBlock, bool kVec>
-__global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 256) k_rmsnorm_residual(const NormArgs a) {
+__global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8)
+    k_rmsnorm_residual(const NormArgs a) {
   constexpr bool k8bit = kOut >= kNormFp8Blk;
-  __shared__ double buf64[k8bit ? 32 : 1];
-  __shared__ float buf32[32];
+  __shared__ SumMax buf64[k8bit ? 2 : 1][k8bit ? 32 : 1];
+  __shared__ float buf32[k8bit ? 1 : 2][k8bit ? 1 : 32];
+  __shared__ unsigned long long s_max[2];
   const int d = a.d, tpr = a.tpr;
   const int t = kBlock ? threadIdx.x : threadIdx.x & (tpr - 1);
   const int rpb = kBlock ? 1 : blockDim.x / tpr;
-  float w[kNormV][8];
+  float2 w[kNormV][4];
 #pragma unroll
   for (int j = 0; j < kNormV; ++j) {
     if (a.w_bf16) norm_load<bf16, kVec>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
     else norm_load<float, kVec>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
   }
+  if (kOut == kNormFp8Row && kBlock && threadIdx.x == 0) s_max[0] = 0ull;
+  int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.n_rows;
-       base += static_cast<int64_t>(gridDim.x) * rpb) {
+       base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
     const int64_t row = base + (kBlock ? 0 : threadIdx.x / tpr);
     const bool live = row < a.n_rows;
     const int64_t at = (live ? row : 0) * d;
-    float h[kNormV][8];
+    float2 h[kNormV][4];
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) norm_load<Tx, kVec>(static_cast<const Tx*>(a.x) + at, j, t, tpr, d, h[j]);
     if (a.r != nullptr) {
+      float2 r[kNormV][4];
+#pragma unroll
+      for (int j = 0; j < kNormV; ++j) norm_load<Tr, kVec>(static_cast<const Tr*>(a.r) + at, j, t, tpr, d, r[j]);
 #pragma unroll
       for (int j = 0; j < kNormV; ++j) {
-        float r[8];
-        norm_load<Tr, kVec>(static_cast<const Tr*>(a.r) + at, j, t, tpr, d, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = round_to<Tr>(h[j][i] + r[i]);
+        for (int i = 0; i < 4; ++i) {
+          h[j][i] = add2(h[j][i], r[j][i]);
+          h[j][i] = make_float2(round_to<Tr>(h[j][i].x), round_to<Tr>(h[j][i].y));
+        }
         if (live) norm_store<Tr, kVec>(static_cast<Tr*>(a.h) + at, j, t, tpr, d, h[j]);
       }
     }
     if constexpr (!k8bit) {
-      float ss = 0.f;
+      float2 ss = both(0.f);
 #pragma unroll
       for (int j = 0; j < kNormV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-      ss = row_reduce<kBlock>(ss, tpr, buf32, OpSum());
-      const float s = 1.0f / sqrtf(ss / static_cast<float>(d) + a.eps);
+        for (int i = 0; i < 4; ++i) ss = fma2(h[j][i], h[j][i], ss);
+      const float sum = row_reduce<kBlock>(ss.x + ss.y, tpr, buf32[turn], OpSum());
+      const float s = 1.0f / sqrtf(sum / static_cast<float>(d) + a.eps);
       using Ty = std::conditional_t<kOut == kNormF32, float, bf16>;
 #pragma unroll
       for (int j = 0; j < kNormV; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * s * w[j][i];
+        for (int i = 0; i < 4; ++i) h[j][i] = mul2(mul2(h[j][i], both(s)), w[j][i]);
         if (live) norm_store<Ty, kVec>(static_cast<Ty*>(a.y) + at, j, t, tpr, d, h[j]);
       }
     } else {
-      double ss = 0.0;
+      SumMax v{0.0, 0.f};
 #pragma unroll
       for (int j = 0; j < kNormV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const double v = static_cast<double>(h[j][i]);
-          ss = fma(v, v, ss);
+        for (int i = 0; i < 4; ++i) {
+          const double x = static_cast<double>(h[j][i].x), y = static_cast<double>(h[j][i].y);
+          v.sum = fma(x, x, v.sum);
+          v.sum = fma(y, y, v.sum);
+          if (kOut == kNormFp8Row) {
+            const float2 p = mul2(h[j][i], w[j][i]);
+            v.max = fmaxf(v.max, fmaxf(fabsf(p.x), fabsf(p.y)));
+          }
         }
-      ss = row_reduce<kBlock>(ss, tpr, buf64, OpSum());
-      const double s = rsqrt64(ss / d + static_cast<double>(a.eps));
+      const float own = v.max;
+      v = row_reduce<kBlock>(v, tpr, buf64[turn], OpSumMax());
+      const double s = rsqrt64(v.sum / d + static_cast<double>(a.eps));
       uint8_t* codes = static_cast<uint8_t*>(a.y) + at;
       if constexpr (kOut == kNormFp8Blk) {
         int8_t* exps = static_cast<int8_t*>(a.scales) + at / 16;
@@ -264,42 +334,40 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 256) k_rmsnorm_resi
           }
         }
       } else {
-        // The row's largest |h w| exactly: the fp32 products find the
-        // candidates (rounding is monotone), 64 bits hold their products.
-        float mf = 0.f;
-#pragma unroll
-        for (int j = 0; j < kNormV; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mf = fmaxf(mf, fabsf(h[j][i] * w[j][i]));
+        // The row's largest |h w| in 64 bits, from the threads that hold the
+        // largest fp32 product (rounding is monotone); non-negative doubles
+        // order as their bits.
         double m = 0.0;
+        if (own == v.max) {
 #pragma unroll
-        for (int j = 0; j < kNormV; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (fabsf(h[j][i] * w[j][i]) == mf)
-              m = fmax(m, fabs(static_cast<double>(h[j][i]) * static_cast<double>(w[j][i])));
-        m = row_reduce<kBlock>(m, tpr, buf64, OpMax()) * s;
-        // Below 448 * 2^-126 the scale stays the least normal fp32.
-        const float c32 = m > 0.0 ? fmaxf(static_cast<float>(m / 448.0), 1.17549435e-38f) : 1.0f;
-        const double k = s / static_cast<double>(c32);
+          for (int j = 0; j < kNormV; ++j) m = fmax(m, real_max(h[j], w[j]));
+        }
+        if (kBlock) {
+          if (threadIdx.x == 0) s_max[turn ^ 1] = 0ull;  // read by all before this row's first barrier
+          if (own == v.max) atomicMax(&s_max[turn], static_cast<unsigned long long>(__double_as_longlong(m)));
+          __syncthreads();
+          m = __longlong_as_double(static_cast<long long>(s_max[turn]));
+        } else {
+          for (int o = tpr / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        const float c32 = fp8row_scale(m * s);
+        const double k = quotient64(s, c32);
         const float kf = static_cast<float>(k);
         if (live && t == 0) static_cast<float*>(a.scales)[row] = c32;
+        const bool range = kf > 1e-30f && kf < 1e30f && v.max < 1e30f;
 #pragma unroll
         for (int j = 0; j < kNormV; ++j) {
           const int c = norm_col<true>(j, 0, t, tpr);
-          float u[8];
-          bool near = !(kf > 1e-30f && kf < 1e30f && mf < 1e30f);
+          float2 u[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            u[i] = h[j][i] * w[j][i] * kf;
-            near |= e4m3_near_border(u[i]);
+          for (int i = 0; i < 4; ++i) u[i] = mul2(mul2(h[j][i], w[j][i]), both(kf));
+          bool sure;
+          uint2 q = e4m3x8_sure(u, &sure);
+          if (!(sure && range)) {
+            real_products(h[j], w[j], k, u);
+            q = e4m3x8(u);
           }
-          if (near) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              u[i] = to_f32_odd(static_cast<double>(h[j][i]) * static_cast<double>(w[j][i]) * k);
-          }
-          if (live && c < d) *reinterpret_cast<uint2*>(codes + c) = e4m3x8(u);
+          if (live && c < d) *reinterpret_cast<uint2*>(codes + c) = q;
         }
       }
     }
@@ -359,55 +427,61 @@ struct NormGradArgs {
 // One pass over the rows; a thread keeps the sums of its columns of dw over all
 // rows it meets in registers and writes them to its row group's slot, so dw is
 // the same on every run (k_sum_slots adds the slots in a fixed order).
+// All of a row's loads go out before the first sum.
 template <typename T, typename Tdy, bool kBlock, bool kVec>
-__global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 256) k_rmsnorm_residual_backward(const NormGradArgs a) {
-  __shared__ float buf[2][32];
+__global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_residual_backward(const NormGradArgs a) {
+  __shared__ float2 buf[2][32];
   const int d = a.d, tpr = a.tpr;
   const int t = kBlock ? threadIdx.x : threadIdx.x & (tpr - 1);
   const int rpb = kBlock ? 1 : blockDim.x / tpr;
   const int group = kBlock ? 0 : threadIdx.x / tpr;
-  float w[kNormV][8], acc[kNormV][8];
+  float2 w[kNormV][4], acc[kNormV][4];
 #pragma unroll
   for (int j = 0; j < kNormV; ++j) {
     if (a.w_bf16) norm_load<bf16, kVec>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
     else norm_load<float, kVec>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
   }
+  int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.n_rows;
-       base += static_cast<int64_t>(gridDim.x) * rpb) {
+       base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
     const int64_t row = base + group;
     const bool live = row < a.n_rows;
     const int64_t at = (live ? row : 0) * d;
-    float h[kNormV][8], g[kNormV][8];
-    float ss = 0.f, dot = 0.f;
+    float2 h[kNormV][4], g[kNormV][4], o[kNormV][4];
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) {
       norm_load<T, kVec>(static_cast<const T*>(a.h) + at, j, t, tpr, d, h[j]);
       norm_load<Tdy, kVec>(static_cast<const Tdy*>(a.dy) + at, j, t, tpr, d, g[j]);
+      if (a.dh != nullptr) {
+        norm_load<T, kVec>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = both(0.f);
+      }
     }
+    float2 ss = both(0.f), dot = both(0.f);
 #pragma unroll
     for (int j = 0; j < kNormV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(h[j][i], h[j][i], ss);
-        dot = fmaf(g[j][i] * w[j][i], h[j][i], dot);
+      for (int i = 0; i < 4; ++i) {
+        ss = fma2(h[j][i], h[j][i], ss);
+        dot = fma2(mul2(g[j][i], w[j][i]), h[j][i], dot);
       }
-    ss = row_reduce<kBlock>(ss, tpr, buf[0], OpSum());
-    dot = row_reduce<kBlock>(dot, tpr, buf[1], OpSum());
-    const float s = 1.0f / sqrtf(ss / static_cast<float>(d) + a.eps);
-    const float corr = dot / static_cast<float>(d) * s * s * s;
+    const float2 sums = row_reduce<kBlock>(make_float2(ss.x + ss.y, dot.x + dot.y), tpr, buf[turn], OpSum2());
+    const float s = 1.0f / sqrtf(sums.x / static_cast<float>(d) + a.eps);
+    const float corr = sums.y / static_cast<float>(d) * s * s * s;
+    const float s_acc = live ? s : 0.f;
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) {
-      float o[8];
-      if (a.dh != nullptr) norm_load<T, kVec>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (live) acc[j][i] = fmaf(g[j][i] * s, h[j][i], acc[j][i]);
-        const float own = g[j][i] * w[j][i] * s - h[j][i] * corr;
-        o[i] = a.dh != nullptr ? o[i] + own : own;
+      for (int i = 0; i < 4; ++i) {
+        acc[j][i] = fma2(mul2(g[j][i], both(s_acc)), h[j][i], acc[j][i]);
+        const float2 own = fma2(h[j][i], both(-corr), mul2(mul2(g[j][i], w[j][i]), both(s)));
+        o[j][i] = add2(o[j][i], own);
       }
-      if (live) norm_store<T, kVec>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o);
+      if (live) norm_store<T, kVec>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o[j]);
     }
   }
   float* slot = a.part + (static_cast<int64_t>(blockIdx.x) * rpb + group) * d;
@@ -422,8 +496,17 @@ static __global__ void __launch_bounds__(1024) k_sum_slots(const float* __restri
   __shared__ float buf[32][33];
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float v = 0.f;
-  if (c < n)
-    for (int64_t s = threadIdx.y; s < slots; s += 32) v += part[s * n + c];
+  if (c < n) {
+    int64_t s = threadIdx.y;
+    for (; s + 7 * 32 < slots; s += 8 * 32) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = part[(s + 32 * i) * n + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += f[i];
+    }
+    for (; s < slots; s += 32) v += part[s * n + c];
+  }
   buf[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   for (int o = 16; o > 0; o >>= 1) {
