@@ -21,7 +21,8 @@ namespace sdm {
 
 constexpr int kClipTensors = 384;  // tensors of one launch (their table is about 10 KB of parameters)
 constexpr int kClipThreads = 256;
-constexpr int kClipVec = 8;        // values of a thread's access
+constexpr int kClipVec = 8;        // values of a thread's access when summing
+constexpr int kClipPerSm = 6;      // blocks of an SM; the grids are whole multiples of what is resident
 
 struct ClipTable {
   const void* grad[kClipTensors];
@@ -100,7 +101,7 @@ __device__ __forceinline__ double clip_chunk_sum(const T* g, int64_t n, bool vec
   return acc;
 }
 
-static __global__ void __launch_bounds__(kClipThreads) k_grad_norm(const __grid_constant__ ClipTable t,
+static __global__ void __launch_bounds__(kClipThreads, kClipPerSm) k_grad_norm(const __grid_constant__ ClipTable t,
                                                                   double* __restrict__ slots) {
   __shared__ double buf[kClipThreads / kWarp];
   double acc = 0.0;
@@ -116,28 +117,32 @@ static __global__ void __launch_bounds__(kClipThreads) k_grad_norm(const __grid_
   if (threadIdx.x == 0) slots[blockIdx.x] = acc;
 }
 
+// A thread's access is at most 16 bytes on either side, so that neighbouring
+// threads' accesses touch (8 values of bf16 into fp32 would leave every other
+// 16 bytes to a second store).
 template <typename T, typename To>
 __device__ __forceinline__ void clip_chunk_scale(const T* g, To* out, int64_t n, bool vec, float c) {
-  constexpr int kStep = kClipThreads * kClipVec;
+  constexpr int kV = sizeof(T) == 2 && sizeof(To) == 2 ? 8 : 4;
+  constexpr int kStep = kClipThreads * kV, kAhead = 64 / (kV * static_cast<int>(sizeof(T)));
   int64_t i = 0;
   if (vec) {
-    for (; i + 4 * kStep <= n; i += 4 * kStep) {
-      float v[4][kClipVec];
+    for (; i + kAhead * kStep <= n; i += kAhead * kStep) {
+      float v[kAhead][kV];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load8<T>(g + i + u * kStep + threadIdx.x * kClipVec, v[u]);
+      for (int u = 0; u < kAhead; ++u) load_unit<T, kV>(g + i + u * kStep + threadIdx.x * kV, v[u]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int k = 0; k < kClipVec; ++k) v[u][k] *= c;
-        store8<To>(out + i + u * kStep + threadIdx.x * kClipVec, v[u]);
+        for (int k = 0; k < kV; ++k) v[u][k] *= c;
+        store_unit<To, kV>(out + i + u * kStep + threadIdx.x * kV, v[u]);
       }
     }
     for (; i + kStep <= n; i += kStep) {
-      float v[kClipVec];
-      load8<T>(g + i + threadIdx.x * kClipVec, v);
+      float v[kV];
+      load_unit<T, kV>(g + i + threadIdx.x * kV, v);
 #pragma unroll
-      for (int k = 0; k < kClipVec; ++k) v[k] *= c;
-      store8<To>(out + i + threadIdx.x * kClipVec, v);
+      for (int k = 0; k < kV; ++k) v[k] *= c;
+      store_unit<To, kV>(out + i + threadIdx.x * kV, v);
     }
   }
   for (i += threadIdx.x; i < n; i += kClipThreads) out[i] = from_f32<To>(to_f32<T>(g[i]) * c);
@@ -145,7 +150,7 @@ __device__ __forceinline__ void clip_chunk_scale(const T* g, To* out, int64_t n,
 
 // norm (written by the first block when given), then out = c g for this
 // launch's tensors. A tensor that is its own output is left alone where c = 1.
-static __global__ void __launch_bounds__(kClipThreads) k_grad_clip(const __grid_constant__ ClipTable t,
+static __global__ void __launch_bounds__(kClipThreads, kClipPerSm) k_grad_clip(const __grid_constant__ ClipTable t,
                                                                   const double* __restrict__ slots, int n_slots,
                                                                   float max_norm, float eps,
                                                                   float* __restrict__ norm_out) {

@@ -9,7 +9,7 @@
 // and neighbouring threads read neighbouring units; the loads of a few tokens go
 // out together one such step before they are used (all of a run's loads at once
 // took the registers of the threads that should have hidden them: 215 us instead
-// of @@CONV@@ for a padded batch of 6 x 4099 x 4096 in bf16).
+// of 56 for a padded batch of 6 x 4099 x 4096 in bf16).
 #pragma once
 
 #include <type_traits>

@@ -11,7 +11,7 @@ namespace sdm_host {
 
 namespace {
 
-constexpr int kClipBlocks = 148 * 8;  // at most: eight blocks of 256 on each SM of a B200
+constexpr int kClipBlocks = 148 * sdm::kClipPerSm;  // at most: what the SMs of a B200 hold at once
 
 struct ClipPlan {
   int64_t total = 0;  // values

@@ -6,8 +6,8 @@ namespace sdm_host {
 
 namespace {
 
-// Tokens a sequence may have for the kernel that keeps nothing but four states
-// a thread: there its tokens are a serial chain of loads.
+// Tokens a sequence may have for the kernel without shared memory: there each
+// token waits for its own loads.
 constexpr int kStepTokens = 4;
 // A split of the token axis has at least this many tokens: its map costs the
 // bandwidth of about 30.
@@ -52,12 +52,14 @@ void launch_sel(const sdm::SelScanArgs& a, int B, cudaStream_t st) {
 
 template <typename T>
 void launch_step(const sdm::SelScanArgs& a, int B, cudaStream_t st) {
-  const int64_t channels = static_cast<int64_t>(B) * a.D;
-  auto grid = [&](int lanes) { return static_cast<unsigned>(ceil_div(channels * lanes, 256)); };
-  if (a.N <= 8) sdm::k_selective_scan_step<T, 2><<<grid(2), 256, 0, st>>>(a, channels);
-  else if (a.N <= 16) sdm::k_selective_scan_step<T, 4><<<grid(4), 256, 0, st>>>(a, channels);
-  else if (a.N <= 32) sdm::k_selective_scan_step<T, 8><<<grid(8), 256, 0, st>>>(a, channels);
-  else sdm::k_selective_scan_step<T, 16><<<grid(16), 256, 0, st>>>(a, channels);
+  const int threads = sdm::kStepThreads;
+  auto grid = [&](int lanes) {
+    return dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.D) * lanes, threads)), B);
+  };
+  if (a.N <= 8) sdm::k_selective_scan_step<T, 8, 1><<<grid(1), threads, 0, st>>>(a);
+  else if (a.N <= 16) sdm::k_selective_scan_step<T, 16, 1><<<grid(1), threads, 0, st>>>(a);
+  else if (a.N <= 32) sdm::k_selective_scan_step<T, 16, 2><<<grid(2), threads, 0, st>>>(a);
+  else sdm::k_selective_scan_step<T, 16, 4><<<grid(4), threads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -98,8 +100,8 @@ sdm_status_t check_selscan(const sdm_selscan_shape_t* s) {
     return fail(SDM_ERR_INVALID_ARGUMENT, "b_stride and c_stride must be 0 or at least G * N");
   if (s->B > 65535) return fail(SDM_ERR_UNSUPPORTED, "B above 65535");
   if (s->T > INT32_MAX - 4096) return fail(SDM_ERR_UNSUPPORTED, "T above 2^31 - 4096");
-  // Block numbers along the channels are 32-bit, and so is a thread's channel.
-  if (static_cast<int64_t>(s->D) * s->B > (int64_t{1} << 34)) return fail(SDM_ERR_UNSUPPORTED, "B * D above 2^34");
+  // Thread numbers along the channels are 32-bit (4 lanes a channel at most).
+  if (s->D > (1 << 26)) return fail(SDM_ERR_UNSUPPORTED, "D above 2^26");
   return SDM_OK;
 }
 
