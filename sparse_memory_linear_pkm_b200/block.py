@@ -10,14 +10,16 @@ and batch rows.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import math
-import struct
+import operator
 
 import torch
 
 from . import native
 
+_dtype = operator.attrgetter("dtype")
 _CODE = {torch.float32: native.F32, torch.bfloat16: native.BF16}
 _OUT = {"f32": native.F32, "bf16": native.BF16, "fp8blk": native.FP8_B16, "fp8row": native.FP8_ROW}
 
@@ -54,7 +56,7 @@ def _at(t: torch.Tensor | None, what: str, dev: int, shape=None, dtype=None, con
 
 def _call(dev: int, fn, *args) -> None:
     """Enqueues a library call on the current stream of dev, whichever device is current."""
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -338,23 +340,26 @@ def grad_norm_clip(grads, max_norm: float, eps: float = 1e-6, out=None) -> torch
     table = [0] * (4 * len(at))  # an array of sdm_grad_tensor_t
     table[::4], table[1::4], table[2::4] = at, out_at, sizes
     table[3::4] = [a | b << 32 for a, b in zip(codes, out_codes)]
+    packed = array.array("q", table)
     lib = native.load()
     ws_bytes = lib.sdm_grad_norm_clip_workspace_bytes(len(at))
     ws = _workspace(ws_bytes, grads[0])
     norm = grads[0].new_empty((), dtype=torch.float32)
-    _call(dev, lib.sdm_grad_norm_clip, struct.pack(f"={len(table)}q", *table), len(at), max_norm, eps, norm.data_ptr(),
+    _call(dev, lib.sdm_grad_norm_clip, packed.buffer_info()[0], len(at), max_norm, eps, norm.data_ptr(),
           ws.data_ptr(), ws_bytes)
     return norm
 
 
 def _flat(tensors, dev: int, what: str):
     """Addresses, type codes and sizes of contiguous tensors on dev."""
-    try:
-        codes = [_CODE[t.dtype] for t in tensors]
-    except KeyError:
-        i = next(i for i, t in enumerate(tensors) if t.dtype not in _CODE)
-        raise TypeError(f"{what} {i} must be float32 or bfloat16, got {tensors[i].dtype}") from None
-    if not all([t.is_contiguous() and t.get_device() == dev for t in tensors]):
+    T = torch.Tensor
+    if set(map(T.get_device, tensors)) != {dev} or not all(map(T.is_contiguous, tensors)):
         i = next(i for i, t in enumerate(tensors) if not (t.is_contiguous() and t.get_device() == dev))
         raise ValueError(f"{what} {i} must be contiguous and on cuda:{dev}")
-    return [t.data_ptr() for t in tensors], codes, [t.numel() for t in tensors]
+    types = list(map(_dtype, tensors))
+    kinds = set(types)
+    if not kinds <= _CODE.keys():
+        i = next(i for i, t in enumerate(types) if t not in _CODE)
+        raise TypeError(f"{what} {i} must be float32 or bfloat16, got {types[i]}")
+    codes = [_CODE[types[0]]] * len(types) if len(kinds) == 1 else [_CODE[t] for t in types]
+    return list(map(T.data_ptr, tensors)), codes, list(map(T.numel, tensors))
