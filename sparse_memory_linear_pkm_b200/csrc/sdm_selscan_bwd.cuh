@@ -1,464 +1,558 @@
 // Gradient of the selective state space scan (sm_100a).
 //
-// With e_t = dy_t silu(z_t), a_t = exp(delta_t A), u_t = a_t h_{t-1}:
+// With e_t = dy_t silu(z_t), a_t = exp(delta_t A), u_t = a_t h_{t-1}, w = delta x:
 //   g_t   = C_t e_t + q_{t+1},  q_t = a_t g_t       (q_{T} = dL/dh_T, q_0 = dL/dh_0)
-//   dC_t  = sum_d e_t h_t            dB_t = sum_d g_t delta_t x_t
+//   dC_t  = sum_d e_t h_t            dB_t = sum_d g_t w_t
 //   p_t   = sum_n g_t B_t            r_t  = sum_n g_t A u_t
 //   dx_t  = delta_t p_t + D e_t      ddelta_t = x_t p_t + r_t
 //   dA    = sum_t g_t delta_t u_t    dD = sum_t e_t x_t
 //   ddt_t = ddelta_t sigmoid(dt_t + bias),  dbias = sum_t ddt_t
 //   dz_t  = dy_t (C_t.h_t + D x_t) silu'(z_t)
 //
-// h is not kept by the forward: its first two launches on splits of one tile
-// give the state before every tile of tokens, and this one walks the tiles from
-// the last to the first. A lane holds four states of one channel; warps along
-// time hold segments with their exponentials (and u) in registers. One
-// run over a segment gives its maps in both directions, h -> P h + H and
-// q -> P q + Q, which a thread per (channel, state) chains over the segments.
+// Three launches over splits of the token axis, a lane holding KS states of one
+// channel as in the forward:
+//   1. maps: each split from zero states, in one walk: h -> P h + H, q -> P q +
+//      R, and, every kGradTile tokens, the state so far and the sum of delta;
+//   2. chain: the states before and the q behind each split;
+//   3. gradient: the tiles of a split from the last to the first. A tile's start
+//      state is its kept local state plus the split's start state times its
+//      decay; the tile is walked forward (u to shared memory, a thread's own) and
+//      backward with its exponentials made again.
+// So every exponential is made three times and nothing else is: that, the
+// exchanges of the sums over channels and the issue slots are about equally
+// loaded. (Four states a lane with segments over warps: 1223 us instead of
+// @@GRAD@@ for B = 2, T = 4096, D = 2048, N = 16 in bf16.)
 //
-// The sums over channels (dB, dC) are taken over a warp's channels by halving
-// exchanges, over the block's groups in shared memory, and over blocks by a
-// second kernel from fp32 partial sums, all in a fixed order: no atomics.
+// The sums over channels (dB, dC) are taken over a warp by halving exchanges,
+// over a block's warps in shared memory, and over blocks by k_selective_scan_sums
+// from fp32 partial sums, all in a fixed order: no atomics.
 #pragma once
 
 #include "sdm_selscan.cuh"
 
 namespace sdm {
 
+constexpr int kGradTile = 4;  // tokens between kept states
+
 struct SelGradArgs {
-  SelScanArgs f;          // the forward's inputs
-  const float* ckpt;      // states before the tiles [B, tiles, D, N]
+  SelScanArgs f;          // the forward's inputs; splits and tokens_per_split (whole tiles)
+  const float* h0;        // [B, D, N] or nullptr
   const void* dy;         // [B, T, D]
   const float* dstate;    // dL/dh_T [B, D, N] or nullptr
+  // Arrays of states hold four states a float4: [.., NP / 4, D].
+  float4* P;              // [B, splits, NP / 4, D] decays
+  float4* H;              // states: the maps', then those before the splits
+  float4* R;              // q: the maps', then those behind the splits
+  float4* kept;           // [B, tiles, NP / 4, D] local states before the tiles
+  float* sums;            // [B, tiles, D] sums of delta before the tiles
+  int tiles;              // of a sequence
   void* dx;               // [B, T, D]
   void* ddt;              // [B, T, D]
   void* dz;               // [B, T, D] with z
+  float* dstate0;         // [B, D, N] or nullptr
   float* part_B;          // [tiles_per_group, B, T, G, N]
   float* part_C;
-  float* part_A;          // [B, D, N]
-  float* part_D;          // [B, D]
-  float* part_bias;       // [B, D]
-  float* dstate0;         // [B, D, N] or nullptr
+  float4* part_A;         // [B * splits, NP / 4, D]
+  float* part_D;          // [2, B * splits, D]: of dD, then of dbias
 };
 
-template <int L, int S, int W, int CG>
-struct SelTile {
-  static constexpr int kThreads = 32 * W * CG;
-  static constexpr int NP = 4 * L;             // states a channel is padded to
-  static constexpr int CW = 32 / L;            // channels of a warp
-  static constexpr int CH = CW * CG;           // channels of a block
-  static constexpr int TT = S * W;             // tokens of a tile
-  static constexpr int I = S / L;              // (token, channel) items per thread
-  static constexpr int V = I >= 4 ? 4 : (I >= 2 ? 2 : 1);
-  static constexpr int UR = CH / V;            // channel units of a token row
-  static constexpr int U = (TT * UR + kThreads - 1) / kThreads;
-  static constexpr int UB = (TT * L + kThreads - 1) / kThreads;  // 4-state units of B (and of C)
+// What one block's threads share: their channels and token range.
+struct SelPlace {
+  int b, split, group, tile_c, c, t_begin, t_end, t_stop;  // t_stop: of the split, padding included
+  bool live;
 };
-
-// Sums over the L lanes of each channel (lane bits below log2 L) of L values:
-// lane j (of a channel) returns the total of v[j].
 template <int L>
-__device__ __forceinline__ float sum_to_lane(float (&v)[L]) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o];
-      const float keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
+__device__ __forceinline__ SelPlace sel_place(const SelScanArgs& a) {
+  SelPlace p;
+  p.split = blockIdx.y;
+  p.b = blockIdx.z;
+  p.group = blockIdx.x / a.tiles_per_group;
+  p.tile_c = blockIdx.x % a.tiles_per_group;
+  const int Dg = a.D / a.G, c = p.group * Dg + p.tile_c * (kSelThreads / L) + threadIdx.x / L;
+  p.live = c < (p.group + 1) * Dg;
+  p.c = min(c, (p.group + 1) * Dg - 1);
+  p.t_begin = p.split * a.tokens_per_split;
+  p.t_stop = min(a.T, p.t_begin + a.tokens_per_split);
+  p.t_end = min(clamp_length(a.lengths, p.b, a.T, a.err), p.t_stop);
+  return p;
 }
 
-template <int L, int S, int W, int CG>
-struct SelGradTile : SelTile<L, S, W, CG> {
-  using Base = SelTile<L, S, W, CG>;
-  static constexpr int kPairs = Base::CH * Base::NP;   // (channel, state) pairs of a block
-  static constexpr int Q = Base::CW > 4 ? Base::CW : 4;  // values of one exchange over channels
-  static constexpr int SB = Q / 4;                       // tokens they cover
-  static constexpr int kSmemFloats = 2 * Base::TT * Base::CH + 2 * Base::TT * Base::NP + 4 * Base::TT * Base::CH +
-                                     2 * CG * Base::TT * Base::NP + 3 * W * kPairs + kPairs;
+// B and C of kGradTile tokens: at most one four-state unit a thread (the first
+// NP threads B's, the next NP C's), loaded a tile before it is written.
+template <typename T, int NP>
+struct GradBC {
+  Raw4<T> raw;
+  const T* base;
+  int64_t stride;
+  int row, n, first;
+  bool in;
+  __device__ __forceinline__ void init(const SelScanArgs& a, const SelPlace& p) {
+    const int tid = threadIdx.x, i = tid % NP;
+    in = tid < 2 * NP;
+    const bool is_c = tid >= NP;
+    row = i / (NP / 4);
+    n = i % (NP / 4) * 4;
+    stride = is_c ? a.c_stride : a.b_stride;
+    base = static_cast<const T*>(is_c ? a.Cm : a.Bm) + static_cast<int64_t>(p.b) * a.T * stride + p.group * a.N + n;
+  }
+  __device__ __forceinline__ void fetch(const SelScanArgs& a, int t0, int t_begin, int t_end) {
+    const int t = t0 + row;
+    raw.load(base + t * stride, a.vec_b, in && t >= t_begin && t < t_end ? a.N - n : 0);
+  }
+  __device__ __forceinline__ void stage(float4* s) const {  // [B, C][kGradTile][NP / 4]
+    if (in) s[threadIdx.x] = raw.get();
+  }
 };
 
-// Sums of Q values over the warp's 32 / L channels (lane bits from log2 L up):
-// the lane of channel j returns values j Q / CW ... in v[0 .. Q / CW).
-template <int L, int Q>
-__device__ __forceinline__ void sum_over_channels(float (&v)[Q]) {
-  const int lane = lane_id();
-  int n = Q;
+// x, dt, z and dy of kGradTile tokens, loaded a tile before they are used.
+template <typename T>
+struct GradRows {
+  RawOne<T> x[kGradTile], d[kGradTile], z[kGradTile], dy[kGradTile];
+  __device__ __forceinline__ void fetch(const SelScanArgs& a, const void* gdy, const SelPlace& p, int t0) {
+    const int64_t row = static_cast<int64_t>(p.b) * a.T + t0;
+    const T* gx = static_cast<const T*>(a.x) + row * a.x_stride + p.c;
+    const T* gd = static_cast<const T*>(a.dt) + row * a.dt_stride + p.c;
+    const T* gz = static_cast<const T*>(a.z) + row * a.z_stride + p.c;
+    const T* gy = static_cast<const T*>(gdy) + row * a.D + p.c;
 #pragma unroll
-  for (int o = 16; o >= L; o >>= 1) {
-    n /= 2;
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < Q / 2; ++i) {
-      if (i < n) {
-        const float send = up ? v[i] : v[i + n];
-        const float keep = up ? v[i + n] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    for (int i = 0; i < kGradTile; ++i) {
+      if (t0 + i >= p.t_begin && t0 + i < p.t_end) {
+        x[i].load(gx + i * a.x_stride);
+        d[i].load(gd + i * a.dt_stride);
+        if (a.z != nullptr) z[i].load(gz + i * a.z_stride);
+        dy[i].load(gy + static_cast<int64_t>(i) * a.D);
       }
     }
   }
+};
+
+template <int KS>
+__device__ __forceinline__ void load_row_states(const float* row, int n0, int N, float2* out) {
+#pragma unroll
+  for (int k = 0; k < KS / 2; k += 2) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (row != nullptr) load_states(row, n0 + 2 * k, N, v);
+    out[k] = make_float2(v[0], v[1]);
+    out[k + 1] = make_float2(v[2], v[3]);
+  }
 }
 
-template <typename T, int L, int S, int W, int CG>
-__global__ void __launch_bounds__(32 * W * CG) k_selective_scan_backward(const SelGradArgs ga) {
-  using Tile = SelGradTile<L, S, W, CG>;
-  constexpr int NP = Tile::NP, CW = Tile::CW, CH = Tile::CH, TT = Tile::TT, V = Tile::V, UR = Tile::UR;
-  constexpr int kThreads = Tile::kThreads, kPairs = Tile::kPairs, Q = Tile::Q, SB = Tile::SB;
-  static_assert(S % L == 0 && S % SB == 0, "exchanges cover whole runs of tokens");
-  static_assert(kThreads % UR == 0, "a thread's items share their channels");
-  extern __shared__ float4 smem4[];
+// ------------------------------------------------------------------- 1. maps --
+
+template <typename T, int KS, int L>
+__global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad_maps(const SelGradArgs ga) {
+  constexpr int NP = KS * L, KP = KS / 2, NG = NP / 4;
+  __shared__ float4 s_bc[2][2 * NP];
   const SelScanArgs& a = ga.f;
-  float2* s_dx = reinterpret_cast<float2*>(smem4);        // [TT][CH] (delta, delta x)
-  float* s_B = reinterpret_cast<float*>(s_dx + TT * CH);  // [TT][NP]
-  float* s_C = s_B + TT * NP;                             // [TT][NP]
-  float* s_e = s_C + TT * NP;                             // [TT][CH]
-  float* s_y = s_e + TT * CH;                             // [TT][CH] sum_n C h
-  float* s_p = s_y + TT * CH;                             // [TT][CH]
-  float* s_r = s_p + TT * CH;                             // [TT][CH]
-  float* s_dB = s_r + TT * CH;                            // [CG][TT][NP]
-  float* s_dC = s_dB + CG * TT * NP;                      // [CG][TT][NP]
-  float* s_P = s_dC + CG * TT * NP;                       // [W][CH][NP]
-  float* s_H = s_P + W * kPairs;                          // [W][CH][NP] map, then state before the segment
-  float* s_Q = s_H + W * kPairs;                          // [W][CH][NP] map, then q after the segment
-  float* s_q = s_Q + W * kPairs;                          // [CH][NP] q after the tile
-
-  const int tid = threadIdx.x, lane = lane_id(), warp = tid / kWarp;
-  const int wt = warp % W, cg = warp / W;
-  const int b = blockIdx.z;
-  const int group = blockIdx.x / a.tiles_per_group, tile_c = blockIdx.x % a.tiles_per_group;
-  const int Dg = a.D / a.G, c0 = group * Dg + tile_c * CH, c_end = (group + 1) * Dg;
-  const int len = clamp_length(a.lengths, b, a.T, a.err);
-  const int tiles = (a.T + TT - 1) / TT;
-
-  const int ch = cg * CW + lane / L, n0 = 4 * (lane % L);
-  const bool live = c0 + ch < c_end;
-  const int64_t c = live ? c0 + ch : c0;
-  float A2[4], dA[4] = {0.f, 0.f, 0.f, 0.f};
-  load_states(a.A + c * a.N, n0, a.N, A2);
+  const SelPlace p = sel_place<L>(a);
+  const int g0 = static_cast<int>(threadIdx.x % L) * (KS / 4);  // first four-state group
+  float2 A2[KP], h[KP], R[KP], P[KP];
+  load_row_states<KS>(a.A + static_cast<int64_t>(p.c) * a.N, 4 * g0, a.N, A2);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
-
-  const T* gx = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride;
-  const T* gdt = static_cast<const T*>(a.dt) + static_cast<int64_t>(b) * a.T * a.dt_stride;
-  const T* gz = a.z == nullptr ? nullptr : static_cast<const T*>(a.z) + static_cast<int64_t>(b) * a.T * a.z_stride;
-  const T* gB = static_cast<const T*>(a.Bm) + static_cast<int64_t>(b) * a.T * a.b_stride + group * a.N;
-  const T* gC = static_cast<const T*>(a.Cm) + static_cast<int64_t>(b) * a.T * a.c_stride + group * a.N;
-  const int64_t out0 = static_cast<int64_t>(b) * a.T * a.D;
-  const T* gdy = static_cast<const T*>(ga.dy) + out0;
-
-  // (channel, state) pairs of this thread's chains: the first kPairs chain the
-  // state forward, the others q backward. s_q starts as dL/dh_T.
-  constexpr int kChains = (2 * kPairs + kThreads - 1) / kThreads;
-  auto pair_at = [&](int64_t row, int pair) -> int64_t {  // place in a [.., D, N] array, or -1
-    const int pc = pair / NP, n = pair % NP;
-    return c0 + pc < c_end && n < a.N ? (row * a.D + c0 + pc) * a.N + n : -1;
-  };
-  for (int i = tid; i < kPairs; i += kThreads) {
-    const int64_t at = pair_at(b, i);
-    s_q[i] = ga.dstate != nullptr && at >= 0 ? ga.dstate[at] : 0.f;
+  for (int k = 0; k < KP; ++k) {
+    A2[k] = mul2(A2[k], both(kLog2e));
+    h[k] = R[k] = both(0.f);
+    P[k] = both(1.0f);
   }
-
-  float px[Tile::U][V], pd[Tile::U][V], pz[Tile::U][V], py[Tile::U][V], pB[Tile::UB][4], pC[Tile::UB][4];
-  float ph[kChains];
-  auto fetch = [&](int tile) {
-    const int t0 = tile * TT;
-#pragma unroll
-    for (int u = 0; u < Tile::U; ++u) {
-      const int i = tid + u * kThreads, t = t0 + i / UR, cc = c0 + (i % UR) * V;
-      const int n = (tile >= 0 && i < TT * UR && t < len) ? c_end - cc : 0;
-      load_channels<T, V>(gx + t * a.x_stride + cc, a.vec_x, n, px[u]);
-      load_channels<T, V>(gdt + t * a.dt_stride + cc, a.vec_x, n, pd[u]);
-      load_channels<T, V>(gdy + static_cast<int64_t>(t) * a.D + cc, a.vec_x, n, py[u]);
-      if (gz != nullptr) load_channels<T, V>(gz + t * a.z_stride + cc, a.vec_x, n, pz[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < Tile::UB; ++u) {
-      const int i = tid + u * kThreads, t = t0 + i / L, n = (i % L) * 4;
-      const int left = (tile >= 0 && i < TT * L && t < len) ? a.N - n : 0;
-      load_channels<T, 4>(gB + t * a.b_stride + n, a.vec_b, left, pB[u]);
-      load_channels<T, 4>(gC + t * a.c_stride + n, a.vec_b, left, pC[u]);
-    }
-#pragma unroll
-    for (int j = 0; j < kChains; ++j) {
-      const int i = tid + j * kThreads;
-      ph[j] = 0.f;
-      if (tile >= 0 && t0 < len && i < kPairs) {
-        const int64_t at = pair_at(static_cast<int64_t>(b) * tiles + tile, i);
-        if (at >= 0) ph[j] = ga.ckpt[at];
-      }
-    }
-  };
-
-  float dD[V], dbias[V], bias[V], skip[V];
-  const int my_c = (tid % UR) * V;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const bool in = c0 + my_c + v < c_end;
-    dD[v] = dbias[v] = 0.f;
-    bias[v] = in && a.bias != nullptr ? a.bias[c0 + my_c + v] : 0.f;
-    skip[v] = in && a.Dskip != nullptr ? a.Dskip[c0 + my_c + v] : 0.f;
-  }
-
-  fetch(tiles - 1);
-  for (int tile = tiles - 1; tile >= 0; --tile) {
-    const int t0 = tile * TT;
-    if (t0 >= len) {
-      // Padding only: its inputs get nothing, and q passes through.
-#pragma unroll
-      for (int u = 0; u < Tile::U; ++u) {
-        const int i = tid + u * kThreads, t = t0 + i / UR;
-        const int n = (i < TT * UR && t < a.T) ? c_end - (c0 + my_c) : 0;
-        const float zero[V] = {};
-        const int64_t at = out0 + static_cast<int64_t>(t) * a.D + c0 + my_c;
-        if (n > 0) {
-          store_channels<T, V>(static_cast<T*>(ga.dx) + at, a.vec_x, n, zero);
-          store_channels<T, V>(static_cast<T*>(ga.ddt) + at, a.vec_x, n, zero);
-          if (gz != nullptr) store_channels<T, V>(static_cast<T*>(ga.dz) + at, a.vec_x, n, zero);
-        }
-      }
-      for (int i = tid; i < TT * NP; i += kThreads) {
-        const int t = t0 + i / NP, n = i % NP;
-        if (t < a.T && n < a.N) {
-          const int64_t at =
-              (((static_cast<int64_t>(tile_c) * gridDim.z + b) * a.T + t) * a.G + group) * a.N + n;
-          ga.part_B[at] = 0.f;
-          ga.part_C[at] = 0.f;
-        }
-      }
-      fetch(tile - 1);
-      continue;
-    }
-    // ---- stage
-    float x[Tile::U][V], pre[Tile::U][V], z[Tile::U][V], dy[Tile::U][V], h_ckpt[kChains];
-#pragma unroll
-    for (int u = 0; u < Tile::U; ++u) {
-      const int i = tid + u * kThreads, tt = i / UR;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[u][v] = px[u][v];
-        dy[u][v] = py[u][v];
-        z[u][v] = gz != nullptr ? pz[u][v] : 0.f;
-        pre[u][v] = pd[u][v] + bias[v];
-        float d = 0.f;
-        if (t0 + tt < len && c0 + my_c + v < c_end) d = a.softplus ? softplus2(both(pre[u][v])).x : pre[u][v];
-        if (i < TT * UR) {
-          s_dx[tt * CH + my_c + v] = make_float2(d, d * x[u][v]);
-          s_e[tt * CH + my_c + v] = gz != nullptr ? dy[u][v] * silu2(both(z[u][v])).x : dy[u][v];
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < Tile::UB; ++u) {
-      const int i = tid + u * kThreads;
-      if (i < TT * L) {
-        *reinterpret_cast<float4*>(s_B + i * 4) = make_float4(pB[u][0], pB[u][1], pB[u][2], pB[u][3]);
-        *reinterpret_cast<float4*>(s_C + i * 4) = make_float4(pC[u][0], pC[u][1], pC[u][2], pC[u][3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kChains; ++j) h_ckpt[j] = ph[j];
+  const float bias = a.bias == nullptr ? 0.f : a.bias[p.c];
+  float total = 0.f;
+  GradRows<T> rows;
+  GradBC<T, NP> bc;
+  bc.init(a, p);
+  rows.fetch(a, ga.dy, p, p.t_begin);
+  bc.fetch(a, p.t_begin, p.t_begin, p.t_end);
+  bc.stage(s_bc[0]);
+  bc.fetch(a, p.t_begin + kGradTile, p.t_begin, p.t_end);
+  int buf = 0;
+  for (int t0 = p.t_begin; t0 < p.t_end; t0 += kGradTile, buf ^= 1) {
     __syncthreads();
-    fetch(tile - 1);
-
-    // ---- the segment's maps: h -> P h + H forward, q -> P q + Q backward
-    const float2* dx = s_dx + wt * S * CH + ch;
-    const float* es = s_e + wt * S * CH + ch;
-    const float4* Bs = reinterpret_cast<const float4*>(s_B + wt * S * NP + n0);
-    const float4* Cs = reinterpret_cast<const float4*>(s_C + wt * S * NP + n0);
-    const int seg = (wt * CH + ch) * NP + n0;
-    float e[S][4], u[S][4];
-    {
-      float P[4] = {1.f, 1.f, 1.f, 1.f}, H[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {0.f, 0.f, 0.f, 0.f};
+    bc.stage(s_bc[buf ^ 1]);
+    bc.fetch(a, t0 + 2 * kGradTile, p.t_begin, p.t_end);
+    const float4* sB = s_bc[buf] + g0;
+    const float4* sC = s_bc[buf] + NP + g0;
+    if (p.live) {
+      const int64_t tile = static_cast<int64_t>(p.b) * ga.tiles + t0 / kGradTile;
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const float2 d = dx[s * CH];
-        const float w = es[s * CH];
-        const float4 Bv = Bs[s * L], Cv = Cs[s * L];
-        const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, Ck[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+      for (int k = 0; k < KP; k += 2)
+        ga.kept[(tile * NG + g0 + k / 2) * a.D + p.c] = make_float4(h[k].x, h[k].y, h[k + 1].x, h[k + 1].y);
+      if (g0 == 0) ga.sums[tile * a.D + p.c] = total;
+    }
+    float x[kGradTile], d[kGradTile], e[kGradTile];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e[s][k] = ex2(d.x * A2[k]);
-          P[k] *= e[s][k];
-          H[k] = fmaf(e[s][k], H[k], d.y * Bk[k]);
-          R[k] = fmaf(P[k], Ck[k] * w, R[k]);
+    for (int i = 0; i < kGradTile; i += 2) {
+      const bool on0 = t0 + i < p.t_end, on1 = t0 + i + 1 < p.t_end;
+      float2 u = make_float2(rows.d[i].get() + bias, rows.d[i + 1].get() + bias);
+      if (a.softplus) u = softplus2(u);
+      float2 v = make_float2(rows.dy[i].get(), rows.dy[i + 1].get());
+      if (a.z != nullptr) v = mul2(v, silu2(make_float2(rows.z[i].get(), rows.z[i + 1].get())));
+      d[i] = on0 ? u.x : 0.f;
+      d[i + 1] = on1 ? u.y : 0.f;
+      e[i] = on0 ? v.x : 0.f;
+      e[i + 1] = on1 ? v.y : 0.f;
+      x[i] = on0 ? rows.x[i].get() : 0.f;
+      x[i + 1] = on1 ? rows.x[i + 1].get() : 0.f;
+    }
+    rows.fetch(a, ga.dy, p, t0 + kGradTile);
+#pragma unroll
+    for (int i = 0; i < kGradTile; ++i) {
+      const float2 dd = both(d[i]), w = both(d[i] * x[i]), ee = both(e[i]);
+      total += d[i];
+#pragma unroll
+      for (int k = 0; k < KP; k += 2) {
+        const float4 Bv = sB[i * NG + k / 2], Cv = sC[i * NG + k / 2];
+#pragma unroll
+        for (int m = k; m < k + 2; ++m) {
+          const float2 q = mul2(dd, A2[m]);
+          const float2 at = make_float2(ex2(q.x), ex2(q.y));
+          h[m] = fma2(at, h[m], mul2(w, m == k ? low2(Bv) : high2(Bv)));
+          P[m] = mul2(P[m], at);
+          R[m] = fma2(P[m], mul2(ee, m == k ? low2(Cv) : high2(Cv)), R[m]);
         }
       }
-      *reinterpret_cast<float4*>(s_P + seg) = make_float4(P[0], P[1], P[2], P[3]);
-      *reinterpret_cast<float4*>(s_H + seg) = make_float4(H[0], H[1], H[2], H[3]);
-      *reinterpret_cast<float4*>(s_Q + seg) = make_float4(R[0], R[1], R[2], R[3]);
-    }
-    __syncthreads();
-    // ---- chains over the segments: each map is replaced by what enters it
-#pragma unroll
-    for (int j = 0; j < kChains; ++j) {
-      const int i = tid + j * kThreads;
-      if (i < kPairs) {
-        float hh = h_ckpt[j];
-#pragma unroll
-        for (int v = 0; v < W; ++v) {
-          const float H = s_H[v * kPairs + i];
-          s_H[v * kPairs + i] = hh;
-          hh = fmaf(s_P[v * kPairs + i], hh, H);
-        }
-      } else if (i < 2 * kPairs) {
-        const int pr = i - kPairs;
-        float q = s_q[pr];
-#pragma unroll
-        for (int v = W - 1; v >= 0; --v) {
-          const float R = s_Q[v * kPairs + pr];
-          s_Q[v * kPairs + pr] = q;
-          q = fmaf(s_P[v * kPairs + pr], q, R);
-        }
-        s_q[pr] = q;
-      }
-    }
-    __syncthreads();
-    // ---- forward through the segment: states, dC, y
-    {
-      const float4 h4 = *reinterpret_cast<const float4*>(s_H + seg);
-      float h[4] = {h4.x, h4.y, h4.z, h4.w};
-      float vC[Q], vy[L];
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const float2 d = dx[s * CH];
-        const float w = es[s * CH];
-        const float4 Bv = Bs[s * L], Cv = Cs[s * L];
-        const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, Ck[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
-        float y = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          u[s][k] = e[s][k] * h[k];
-          h[k] = fmaf(d.y, Bk[k], u[s][k]);
-          vC[(s % SB) * 4 + k] = w * h[k];
-          y = fmaf(Ck[k], h[k], y);
-        }
-        vy[s % L] = y;
-        if (s % SB == SB - 1) {
-          sum_over_channels<L, Q>(vC);
-#pragma unroll
-          for (int m = 0; m < Q / CW; ++m) {
-            const int id = (lane / L) * (Q / CW) + m;
-            s_dC[(cg * TT + wt * S + s - (SB - 1) + id / 4) * NP + n0 + id % 4] = vC[m];
-          }
-        }
-        if (gz != nullptr && s % L == L - 1)
-          s_y[(wt * S + s - (L - 1) + lane % L) * CH + ch] = sum_to_lane<L>(vy);
-      }
-    }
-    // ---- backward through it: g, dB, p, r, dA
-    {
-      const float4 q4 = *reinterpret_cast<const float4*>(s_Q + seg);
-      float q[4] = {q4.x, q4.y, q4.z, q4.w};
-      float vB[Q], vp[L], vr[L];
-#pragma unroll
-      for (int s = S - 1; s >= 0; --s) {
-        const float2 d = dx[s * CH];
-        const float w = es[s * CH];
-        const float4 Bv = Bs[s * L], Cv = Cs[s * L];
-        const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, Ck[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
-        float p = 0.f, r = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float g = fmaf(Ck[k], w, q[k]);
-          vB[(s % SB) * 4 + k] = g * d.y;
-          p = fmaf(g, Bk[k], p);
-          const float gu = g * u[s][k];
-          r = fmaf(A2[k], gu, r);
-          dA[k] = fmaf(d.x, gu, dA[k]);
-          q[k] = e[s][k] * g;
-        }
-        vp[s % L] = p;
-        vr[s % L] = r * kLn2;  // A2 = A log2(e)
-        if (s % SB == 0) {
-          sum_over_channels<L, Q>(vB);
-#pragma unroll
-          for (int m = 0; m < Q / CW; ++m) {
-            const int id = (lane / L) * (Q / CW) + m;
-            s_dB[(cg * TT + wt * S + s + id / 4) * NP + n0 + id % 4] = vB[m];
-          }
-        }
-        if (s % L == 0) {
-          s_p[(wt * S + s + lane % L) * CH + ch] = sum_to_lane<L>(vp);
-          s_r[(wt * S + s + lane % L) * CH + ch] = sum_to_lane<L>(vr);
-        }
-      }
-    }
-    __syncthreads();
-    // ---- per (token, channel) and per (token, state) outputs
-#pragma unroll
-    for (int uu = 0; uu < Tile::U; ++uu) {
-      const int i = tid + uu * kThreads, tt = i / UR, t = t0 + tt;
-      const int n = (i < TT * UR && t < a.T) ? c_end - (c0 + my_c) : 0;
-      if (n > 0) {
-        float o_x[V], o_t[V], o_z[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int at = tt * CH + my_c + v;
-          const float p = s_p[at], w = s_e[at], xv = x[uu][v];
-          o_x[v] = o_t[v] = o_z[v] = 0.f;
-          if (t < len && v < n) {
-            o_x[v] = fmaf(s_dx[at].x, p, skip[v] * w);
-            float dd = fmaf(xv, p, s_r[at]);
-            if (a.softplus) dd *= sigmoid2(both(pre[uu][v])).x;
-            o_t[v] = dd;
-            dbias[v] += dd;
-            dD[v] = fmaf(w, xv, dD[v]);
-            if (gz != nullptr) o_z[v] = dy[uu][v] * fmaf(skip[v], xv, s_y[at]) * silu_grad2(both(z[uu][v])).x;
-          }
-        }
-        const int64_t at = out0 + static_cast<int64_t>(t) * a.D + c0 + my_c;
-        store_channels<T, V>(static_cast<T*>(ga.dx) + at, a.vec_x, n, o_x);
-        store_channels<T, V>(static_cast<T*>(ga.ddt) + at, a.vec_x, n, o_t);
-        if (gz != nullptr) store_channels<T, V>(static_cast<T*>(ga.dz) + at, a.vec_x, n, o_z);
-      }
-    }
-    for (int i = tid; i < TT * NP; i += kThreads) {
-      const int t = t0 + i / NP, n = i % NP;
-      if (t < a.T && n < a.N) {
-        float sB = 0.f, sC = 0.f;
-#pragma unroll
-        for (int v = 0; v < CG; ++v) sB += s_dB[v * TT * NP + i], sC += s_dC[v * TT * NP + i];
-        const int64_t at = (((static_cast<int64_t>(tile_c) * gridDim.z + b) * a.T + t) * a.G + group) * a.N + n;
-        ga.part_B[at] = sB;
-        ga.part_C[at] = sC;
-      }
-    }
-    __syncthreads();
-  }
-
-  // ---- sums over the tokens, and q before the first one
-  __syncthreads();
-  *reinterpret_cast<float4*>(s_P + (wt * CH + ch) * NP + n0) = make_float4(dA[0], dA[1], dA[2], dA[3]);
-  float* s_sum = reinterpret_cast<float*>(s_dx);  // [kThreads / UR][CH], twice
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s_sum[(tid / UR) * CH + my_c + v] = dD[v];
-    s_sum[kThreads * V + (tid / UR) * CH + my_c + v] = dbias[v];
-  }
-  __syncthreads();
-  for (int i = tid; i < kPairs; i += kThreads) {
-    const int64_t at = pair_at(b, i);
-    if (at >= 0) {
-      float v = 0.f;
-      for (int w = 0; w < W; ++w) v += s_P[w * kPairs + i];
-      ga.part_A[at] = v;
-      if (ga.dstate0 != nullptr) ga.dstate0[at] = s_q[i];
     }
   }
-  for (int i = tid; i < 2 * CH; i += kThreads) {
-    const int cc = i % CH;
-    if (c0 + cc < c_end) {
-      float v = 0.f;
-      for (int r = 0; r < kThreads / UR; ++r) v += s_sum[(i < CH ? 0 : kThreads * V) + r * CH + cc];
-      (i < CH ? ga.part_D : ga.part_bias)[static_cast<int64_t>(b) * a.D + c0 + cc] = v;
-    }
+  if (!p.live) return;
+  const int64_t at = (static_cast<int64_t>(p.b) * a.splits + p.split) * NG;
+#pragma unroll
+  for (int k = 0; k < KP; k += 2) {
+    const int64_t i = (at + g0 + k / 2) * a.D + p.c;
+    ga.P[i] = make_float4(P[k].x, P[k].y, P[k + 1].x, P[k + 1].y);
+    ga.H[i] = make_float4(h[k].x, h[k].y, h[k + 1].x, h[k + 1].y);
+    ga.R[i] = make_float4(R[k].x, R[k].y, R[k + 1].x, R[k + 1].y);
   }
 }
+
+// ------------------------------------------------------------------ 2. chain --
+
+__device__ __forceinline__ float4 fma4(float4 p, float4 v, float4 q) {
+  const float2 a = fma2(low2(p), low2(v), low2(q)), b = fma2(high2(p), high2(v), high2(q));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// A thread per four states of a channel and batch row walks the splits forward
+// (H becomes the state before each) and backward (R becomes the q behind it).
+static __global__ void __launch_bounds__(128) k_selective_scan_grad_chain(const SelGradArgs ga, int NG) {
+  const SelScanArgs& a = ga.f;
+  const int c = blockIdx.x * blockDim.x + threadIdx.x, g = blockIdx.y, b = blockIdx.z;
+  if (c >= a.D) return;
+  constexpr int kAhead = 4;  // the loads of as many splits go out together
+  const int64_t row = (static_cast<int64_t>(b) * a.D + c) * a.N, step = static_cast<int64_t>(NG) * a.D;
+  const int64_t first = (static_cast<int64_t>(b) * a.splits * NG + g) * a.D + c;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (ga.h0 != nullptr) load_states(ga.h0 + row, 4 * g, a.N, v);
+  float4 h = make_float4(v[0], v[1], v[2], v[3]);
+  v[0] = v[1] = v[2] = v[3] = 0.f;
+  if (ga.dstate != nullptr) load_states(ga.dstate + row, 4 * g, a.N, v);
+  float4 q = make_float4(v[0], v[1], v[2], v[3]);
+  for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
+    float4 P0[kAhead], H0[kAhead], P1[kAhead], R1[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int s = s0 + j;
+      P0[j] = H0[j] = P1[j] = R1[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < a.splits) {
+        P0[j] = ga.P[first + s * step];
+        H0[j] = ga.H[first + s * step];
+        P1[j] = ga.P[first + (a.splits - 1 - s) * step];
+        R1[j] = ga.R[first + (a.splits - 1 - s) * step];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int s = s0 + j;
+      if (s < a.splits) {
+        ga.H[first + s * step] = h;
+        ga.R[first + (a.splits - 1 - s) * step] = q;
+        h = fma4(P0[j], h, H0[j]);
+        q = fma4(P1[j], q, R1[j]);
+      }
+    }
+  }
+  if (ga.dstate0 != nullptr) {
+    const float o[4] = {q.x, q.y, q.z, q.w};
+    store_states(ga.dstate0 + row, 4 * g, a.N, o);
+  }
+}
+
+// --------------------------------------------------------------- 3. gradient --
+
+// Sums of a lane's KS values over the warp's channels (lane bits from log2 L
+// up). Register groups of four values are held in another order in each lane,
+// group j being group j ^ sum_order(lane): what a lane sends in the first
+// exchanges is then always its upper half, with nothing to select. Returns in
+// v[0 .. kLeft) the sums of values kLeft * sum_place(lane) .. of group
+// sum_order(lane); lanes that differ in the remaining bits hold the same.
+template <int KS, int L>
+struct ChannelSum {
+  static constexpr int kOrderBits = KS == 16 ? 2 : 1;          // lane bits 4 (and 3)
+  static constexpr int kLow = L == 1 ? 0 : (L == 2 ? 1 : 2);   // lowest channel bit
+  static constexpr int kBits = 5 - kOrderBits - kLow;          // channel bits left after them
+  static constexpr int kLeft = kBits >= 2 ? 1 : 2;
+  __device__ static __forceinline__ int order(int lane) { return KS == 16 ? lane >> 3 : lane >> 4; }
+  __device__ static __forceinline__ int place(int lane) {
+    const int top = 4 - kOrderBits;  // highest bit left
+    return kBits >= 2 ? (lane >> (top - 1)) & 3 : (lane >> top) & 1;
+  }
+  // One lane of those that hold the same sums.
+  __device__ static __forceinline__ bool writes(int lane) {
+    const int spare = kBits > 2 ? kBits - 2 : 0;
+    return ((lane >> kLow) & ((1 << spare) - 1)) == 0;
+  }
+  __device__ static __forceinline__ float2 over(float2 v, int o) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+  }
+  __device__ static __forceinline__ void run(float2 (&v)[KS / 2]) {
+    const int lane = lane_id();
+    if constexpr (KS == 16) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = add2(v[k], over(v[k + 4], 16));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[k] = add2(v[k], over(v[k + 2], 8));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[k] = add2(v[k], over(v[k + 2], 16));
+    }
+    int o = 1 << (4 - kOrderBits);
+    bool up = lane & o;
+    const float2 send = up ? v[0] : v[1], keep = up ? v[1] : v[0];
+    v[0] = add2(keep, over(send, o));
+    if constexpr (kBits >= 2) {
+      o >>= 1;
+      up = lane & o;
+      const float s1 = up ? v[0].x : v[0].y, k1 = up ? v[0].y : v[0].x;
+      v[0].x = k1 + __shfl_xor_sync(0xffffffffu, s1, o);
+#pragma unroll
+      for (int i = 2; i < kBits; ++i) {
+        o >>= 1;
+        v[0].x += __shfl_xor_sync(0xffffffffu, v[0].x, o);
+      }
+    }
+  }
+};
+
+template <int KS, int L>
+struct GradSmem {
+  static constexpr int NP = KS * L, kWarps = kSelThreads / kWarp;
+  float4 u[kGradTile][KS / 4][kSelThreads];   // a thread's own a_t h_{t-1}
+  float4 item[kGradTile][kSelThreads];        // a thread's own (delta, x, e, sigmoid(dt + bias))
+  float4 bc[2][2 * NP];
+  float sum[2][2][kWarps][kGradTile][NP];     // dB, dC of the warps' channels, two tiles
+};
+
+template <typename T, int KS, int L>
+__global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad(const SelGradArgs ga) {
+  using Smem = GradSmem<KS, L>;
+  using Sum = ChannelSum<KS, L>;
+  constexpr int NP = KS * L, KP = KS / 2, NG = NP / 4, GL = KS / 4;
+  extern __shared__ float4 smem4[];
+  Smem& s = *reinterpret_cast<Smem*>(smem4);
+  const SelScanArgs& a = ga.f;
+  const SelPlace p = sel_place<L>(a);
+  const int tid = threadIdx.x, lane = lane_id(), warp = tid / kWarp;
+  const int g0 = (tid % L) * GL, order = Sum::order(lane);
+  const bool writes = p.live && g0 == 0;
+  float2 A2[KP], q[KP], dA[KP];
+  const int64_t at_split = (static_cast<int64_t>(p.b) * a.splits + p.split) * NG;
+#pragma unroll
+  for (int j = 0; j < GL; ++j) {
+    const int g = g0 + (j ^ order);
+    float v[4];
+    load_states(a.A + static_cast<int64_t>(p.c) * a.N, 4 * g, a.N, v);
+    A2[2 * j] = mul2(make_float2(v[0], v[1]), both(kLog2e));
+    A2[2 * j + 1] = mul2(make_float2(v[2], v[3]), both(kLog2e));
+    const float4 f = ga.R[(at_split + g) * a.D + p.c];
+    q[2 * j] = low2(f);
+    q[2 * j + 1] = high2(f);
+    dA[2 * j] = dA[2 * j + 1] = both(0.f);
+  }
+  const float bias = a.bias == nullptr ? 0.f : a.bias[p.c], skip = a.Dskip == nullptr ? 0.f : a.Dskip[p.c];
+  float sum_D = 0.f, sum_bias = 0.f;
+  const int64_t row0 = static_cast<int64_t>(p.b) * a.T;
+  T* dx = static_cast<T*>(ga.dx) + row0 * a.D + p.c;
+  T* ddt = static_cast<T*>(ga.ddt) + row0 * a.D + p.c;
+  T* dz = a.z == nullptr ? nullptr : static_cast<T*>(ga.dz) + row0 * a.D + p.c;
+
+  // Padding behind the sequence: its inputs get nothing.
+  const int n_tiles = p.t_end > p.t_begin ? (p.t_end - p.t_begin + kGradTile - 1) / kGradTile : 0;
+  for (int t = p.t_begin + n_tiles * kGradTile; t < p.t_stop; ++t) {
+    if (writes) {
+      dx[static_cast<int64_t>(t) * a.D] = from_f32<T>(0.f);
+      ddt[static_cast<int64_t>(t) * a.D] = from_f32<T>(0.f);
+      if (dz != nullptr) dz[static_cast<int64_t>(t) * a.D] = from_f32<T>(0.f);
+    }
+  }
+  // dB and dC of token t, state n: their places in the partial sums.
+  auto part_at = [&](int t, int n) {
+    return (((static_cast<int64_t>(p.tile_c) * gridDim.z + p.b) * a.T + t) * a.G + p.group) * a.N + n;
+  };
+  for (int i = tid; i < (p.t_stop - p.t_begin - n_tiles * kGradTile) * NP; i += kSelThreads) {
+    const int t = p.t_begin + n_tiles * kGradTile + i / NP, n = i % NP;
+    if (n < a.N) ga.part_B[part_at(t, n)] = ga.part_C[part_at(t, n)] = 0.f;
+  }
+
+  GradRows<T> rows;
+  GradBC<T, NP> bc;
+  bc.init(a, p);
+  int t0 = p.t_begin + (n_tiles - 1) * kGradTile;
+  rows.fetch(a, ga.dy, p, t0);
+  bc.fetch(a, t0, p.t_begin, p.t_end);
+  bc.stage(s.bc[0]);
+  bc.fetch(a, t0 - kGradTile, p.t_begin, p.t_end);
+  __syncthreads();
+  int buf = 0;
+  for (int left = n_tiles; left > 0; --left, t0 -= kGradTile, buf ^= 1) {
+    // ---- the state before the tile
+    float2 h[KP];
+    {
+      const int64_t tile = static_cast<int64_t>(p.b) * ga.tiles + t0 / kGradTile;
+      const float2 sum = both(ga.sums[tile * a.D + p.c]);
+#pragma unroll
+      for (int j = 0; j < GL; ++j) {
+        const int g = g0 + (j ^ order);
+        const float4 f = ga.kept[(tile * NG + g) * a.D + p.c], start = ga.H[(at_split + g) * a.D + p.c];
+        const float2 e0 = mul2(sum, A2[2 * j]), e1 = mul2(sum, A2[2 * j + 1]);
+        h[2 * j] = fma2(make_float2(ex2(e0.x), ex2(e0.y)), low2(start), low2(f));
+        h[2 * j + 1] = fma2(make_float2(ex2(e1.x), ex2(e1.y)), high2(start), high2(f));
+      }
+    }
+    // ---- per token: step size, input, gated output gradient
+    float x[kGradTile], d[kGradTile], e[kGradTile], zg[kGradTile];  // zg: dy silu'(z)
+#pragma unroll
+    for (int i = 0; i < kGradTile; i += 2) {
+      const bool on0 = t0 + i < p.t_end, on1 = t0 + i + 1 < p.t_end;
+      const float2 u = make_float2(rows.d[i].get() + bias, rows.d[i + 1].get() + bias);
+      const float2 step = a.softplus ? softplus2(u) : u;
+      // sigmoid(u) = exp(u - softplus(u))
+      float2 sig = both(1.0f);
+      if (a.softplus) sig = make_float2(ex2((u.x - step.x) * kLog2e), ex2((u.y - step.y) * kLog2e));
+      float2 v = make_float2(rows.dy[i].get(), rows.dy[i + 1].get());
+      if (a.z != nullptr) {
+        const float2 z = make_float2(rows.z[i].get(), rows.z[i + 1].get()), gz = sigmoid2(z);
+        const float2 slope = mul2(v, fma2(gz, fma2(make_float2(-gz.x, -gz.y), z, z), gz));
+        zg[i] = slope.x;
+        zg[i + 1] = slope.y;
+        v = mul2(v, mul2(z, gz));
+      }
+      d[i] = on0 ? step.x : 0.f;
+      d[i + 1] = on1 ? step.y : 0.f;
+      e[i] = on0 ? v.x : 0.f;
+      e[i + 1] = on1 ? v.y : 0.f;
+      x[i] = on0 ? rows.x[i].get() : 0.f;
+      x[i + 1] = on1 ? rows.x[i + 1].get() : 0.f;
+      s.item[i][tid] = make_float4(d[i], x[i], e[i], on0 ? sig.x : 0.f);
+      s.item[i + 1][tid] = make_float4(d[i + 1], x[i + 1], e[i + 1], on1 ? sig.y : 0.f);
+    }
+    bc.stage(s.bc[buf ^ 1]);
+    rows.fetch(a, ga.dy, p, t0 - kGradTile);
+    bc.fetch(a, t0 - 2 * kGradTile, p.t_begin, p.t_end);
+    const float4* sB = s.bc[buf] + g0;
+    const float4* sC = s.bc[buf] + NP + g0;
+    const int n_sum = 4 * (g0 + order) + Sum::kLeft * Sum::place(lane);
+    // ---- forward: u, y, dC
+#pragma unroll
+    for (int i = 0; i < kGradTile; ++i) {
+      const float2 dd = both(d[i]), w = both(d[i] * x[i]), ee = both(e[i]);
+      float2 y = both(0.f), v[KP];
+#pragma unroll
+      for (int j = 0; j < GL; ++j) {
+        const float4 Bv = sB[i * NG + (j ^ order)], Cv = sC[i * NG + (j ^ order)];
+        const float2 p0 = mul2(dd, A2[2 * j]), p1 = mul2(dd, A2[2 * j + 1]);
+        const float2 u0 = mul2(make_float2(ex2(p0.x), ex2(p0.y)), h[2 * j]);
+        const float2 u1 = mul2(make_float2(ex2(p1.x), ex2(p1.y)), h[2 * j + 1]);
+        s.u[i][j][tid] = make_float4(u0.x, u0.y, u1.x, u1.y);
+        h[2 * j] = fma2(w, low2(Bv), u0);
+        h[2 * j + 1] = fma2(w, high2(Bv), u1);
+        y = fma2(low2(Cv), h[2 * j], fma2(high2(Cv), h[2 * j + 1], y));
+        v[2 * j] = mul2(ee, h[2 * j]);
+        v[2 * j + 1] = mul2(ee, h[2 * j + 1]);
+      }
+      if (!p.live) {
+#pragma unroll
+        for (int k = 0; k < KP; ++k) v[k] = both(0.f);
+      }
+      Sum::run(v);
+      if (Sum::writes(lane)) {
+        s.sum[buf][1][warp][i][n_sum] = v[0].x;
+        if (Sum::kLeft == 2) s.sum[buf][1][warp][i][n_sum + 1] = v[0].y;
+      }
+      if (dz != nullptr) {
+        float o = y.x + y.y;
+#pragma unroll
+        for (int m = L / 2; m > 0; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+        if (writes && t0 + i < p.t_stop)
+          dz[static_cast<int64_t>(t0 + i) * a.D] = from_f32<T>(t0 + i < p.t_end ? zg[i] * fmaf(skip, x[i], o) : 0.f);
+      }
+    }
+    // ---- backward: g, dB, p, r, dA
+#pragma unroll
+    for (int i = kGradTile - 1; i >= 0; --i) {
+      const float4 it = s.item[i][tid];
+      const float2 dd = both(it.x), w = both(it.x * it.y), ee = both(it.z);
+      float2 pp = both(0.f), rr = both(0.f), v[KP];
+#pragma unroll
+      for (int j = 0; j < GL; ++j) {
+        const float4 Bv = sB[i * NG + (j ^ order)], Cv = sC[i * NG + (j ^ order)], u = s.u[i][j][tid];
+#pragma unroll
+        for (int m = 2 * j; m < 2 * j + 2; ++m) {
+          const bool lo = m == 2 * j;
+          const float2 g = fma2(lo ? low2(Cv) : high2(Cv), ee, q[m]);
+          v[m] = mul2(g, w);
+          pp = fma2(g, lo ? low2(Bv) : high2(Bv), pp);
+          const float2 gu = mul2(g, lo ? low2(u) : high2(u));
+          rr = fma2(A2[m], gu, rr);
+          dA[m] = fma2(dd, gu, dA[m]);
+          const float2 t = mul2(dd, A2[m]);
+          q[m] = mul2(make_float2(ex2(t.x), ex2(t.y)), g);
+        }
+      }
+      if (!p.live) {
+#pragma unroll
+        for (int k = 0; k < KP; ++k) v[k] = both(0.f);
+      }
+      Sum::run(v);
+      if (Sum::writes(lane)) {
+        s.sum[buf][0][warp][i][n_sum] = v[0].x;
+        if (Sum::kLeft == 2) s.sum[buf][0][warp][i][n_sum + 1] = v[0].y;
+      }
+      float ps = pp.x + pp.y, rs = rr.x + rr.y;
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) {
+        ps += __shfl_xor_sync(0xffffffffu, ps, m);
+        rs += __shfl_xor_sync(0xffffffffu, rs, m);
+      }
+      const float du = fmaf(it.y, ps, rs * kLn2) * it.w;  // A2 = A log2(e); sigmoid 0 for padding
+      sum_bias += du;
+      sum_D = fmaf(it.z, it.y, sum_D);
+      if (writes && t0 + i < p.t_stop) {
+        dx[static_cast<int64_t>(t0 + i) * a.D] = from_f32<T>(fmaf(it.x, ps, skip * it.z));
+        ddt[static_cast<int64_t>(t0 + i) * a.D] = from_f32<T>(du);
+      }
+    }
+    // ---- the block's sums over its warps' channels
+    __syncthreads();
+    for (int i = tid; i < 2 * kGradTile * NP; i += kSelThreads) {
+      const int which = i / (kGradTile * NP), r = i % (kGradTile * NP) / NP, n = i % NP;
+      if (n < a.N && t0 + r < p.t_stop) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < Smem::kWarps; ++k) v += s.sum[buf][which][k][r][n];
+        (which == 0 ? ga.part_B : ga.part_C)[part_at(t0 + r, n)] = v;
+      }
+    }
+  }
+  if (!p.live) return;
+  const int64_t slot = static_cast<int64_t>(p.b) * a.splits + p.split;
+#pragma unroll
+  for (int j = 0; j < GL; ++j)
+    ga.part_A[(slot * NG + g0 + (j ^ order)) * a.D + p.c] =
+        make_float4(dA[2 * j].x, dA[2 * j].y, dA[2 * j + 1].x, dA[2 * j + 1].y);
+  if (g0 == 0) {
+    ga.part_D[slot * a.D + p.c] = sum_D;
+    ga.part_D[(static_cast<int64_t>(gridDim.z) * a.splits + slot) * a.D + p.c] = sum_bias;
+  }
+}
+
+// ---------------------------------------------------------------------- sums --
 
 // out[i] = sum over slots of part[slot, i] for i < n, rounded once to T: the
 // channel tiles' sums of dB and dC (blockIdx.y picks which). A thread takes
@@ -487,14 +581,42 @@ __global__ void __launch_bounds__(256) k_selective_scan_sums(const float* __rest
   }
 }
 
-// out[i] = sum over b of part[b, i], in order.
-static __global__ void __launch_bounds__(256) k_selective_scan_batch_sum(const float* __restrict__ part, int B,
-                                                                         int64_t n, float* __restrict__ out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  float v = 0.f;
-  for (int b = 0; b < B; ++b) v += part[b * n + i];
-  out[i] = v;
+// dA [D, N], dD and dbias [D] (nullptr: not wanted) from the blocks' sums, in a
+// fixed order: threadIdx.y takes every eighth slot, then the eight are added.
+// blockIdx.y: a four-state group of dA, then dD and dbias.
+static __global__ void __launch_bounds__(256) k_selective_scan_grad_params(const SelGradArgs ga, int NG, int slots,
+                                                                           float* __restrict__ dA,
+                                                                           float* __restrict__ dD,
+                                                                           float* __restrict__ dbias) {
+  __shared__ float4 buf[8][32];
+  const int D = ga.f.D, c = blockIdx.x * 32 + threadIdx.x, g = blockIdx.y;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < D) {
+#pragma unroll 4
+    for (int s = threadIdx.y; s < slots; s += 8) {
+      if (g < NG) {
+        const float4 f = ga.part_A[(static_cast<int64_t>(s) * NG + g) * D + c];
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+      } else {
+        v.x += ga.part_D[static_cast<int64_t>(s) * D + c];
+        v.y += ga.part_D[static_cast<int64_t>(slots + s) * D + c];
+      }
+    }
+  }
+  buf[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= D) return;
+  for (int r = 1; r < 8; ++r) {
+    const float4 f = buf[r][threadIdx.x];
+    v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+  }
+  if (g < NG) {
+    const float o[4] = {v.x, v.y, v.z, v.w};
+    store_states(dA + static_cast<int64_t>(c) * ga.f.N, 4 * g, ga.f.N, o);
+  } else {
+    if (dD != nullptr) dD[c] = v.x;
+    if (dbias != nullptr) dbias[c] = v.y;
+  }
 }
 
 }  // namespace sdm

@@ -7,58 +7,58 @@ namespace sdm_host {
 
 namespace {
 
-// A gradient block: 64 tokens by 2 channel groups. Segments of 8 tokens (their
-// exponentials and states are 64 registers); the 16 lanes of a wide channel
-// exchange 16 tokens' sums at a time, so those take segments of 16.
-constexpr int kGradTokens = 64, kGradGroups = 2;
-template <int L>
-constexpr int kGradSegment = L == 16 ? 16 : 8;
+constexpr int kGradSplitTokens = 64;  // a split has at least this many tokens
 
 struct SelGradPlan {
-  int ch = 0, tiles = 0, tiles_per_group = 0;
-  size_t ckpt = 0, part_bc = 0, part_A = 0, part_D = 0;
-  size_t total() const { return ckpt + 2 * part_bc + part_A + 2 * part_D; }
+  int NP = 0;                 // states a channel is padded to
+  int splits = 1, tokens_per_split = 0, tiles = 0, tiles_per_group = 0;
+  size_t split_states = 0, kept = 0, sums = 0, part_bc = 0, part_A = 0, part_D = 0;
+  size_t total() const { return 3 * split_states + kept + sums + 2 * part_bc + part_A + part_D; }
 };
 
-// Lanes of a channel in the gradient: four states a lane, two lanes at least.
-int grad_lanes(int32_t N) {
-  int L = 2;
-  while (4 * L < N) L *= 2;
-  return L;
-}
-
+// The token axis is split until 24 warps a SM are there (a split's maps and its
+// start state cost the bandwidth of some 20 tokens), into whole tiles.
 SelGradPlan sel_grad_plan(const sdm_selscan_shape_t& s) {
   SelGradPlan p;
-  p.ch = 32 / grad_lanes(s.N) * kGradGroups;
-  p.tiles = static_cast<int>(ceil_div(s.T, kGradTokens));
-  p.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, p.ch));
-  const size_t f = sizeof(float);
-  p.ckpt = align256(2 * static_cast<size_t>(s.B) * p.tiles * s.D * s.N * f);  // decays, states
+  p.NP = s.N <= 8 ? 8 : (s.N <= 16 ? 16 : (s.N <= 32 ? 32 : 64));
+  p.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, sel_channels(s.N)));
+  p.tiles = static_cast<int>(ceil_div(s.T, sdm::kGradTile));
+  const int64_t warps = static_cast<int64_t>(s.B) * s.G * p.tiles_per_group * (sdm::kSelThreads / 32);
+  const int64_t splits =
+      std::max<int64_t>(1, std::min<int64_t>(ceil_div(24 * kSms, warps), s.T / kGradSplitTokens));
+  p.tokens_per_split = static_cast<int>(ceil_div(ceil_div(s.T, splits), sdm::kGradTile) * sdm::kGradTile);
+  p.splits = static_cast<int>(ceil_div(s.T, p.tokens_per_split));
+  const size_t f = sizeof(float), row = static_cast<size_t>(s.D) * p.NP * f;
+  p.split_states = align256(static_cast<size_t>(s.B) * p.splits * row);
+  p.kept = align256(static_cast<size_t>(s.B) * p.tiles * row);
+  p.sums = align256(static_cast<size_t>(s.B) * p.tiles * s.D * f);
   p.part_bc = align256(static_cast<size_t>(p.tiles_per_group) * s.B * s.T * s.G * s.N * f);
-  p.part_A = align256(static_cast<size_t>(s.B) * s.D * s.N * f);
-  p.part_D = align256(static_cast<size_t>(s.B) * s.D * f);
+  p.part_A = align256(static_cast<size_t>(s.B) * p.splits * row);
+  p.part_D = align256(2 * static_cast<size_t>(s.B) * p.splits * s.D * f);
   return p;
 }
 
-template <typename T, int L>
-sdm_status_t launch_grad_lanes(const SelGradPlan& p, const sdm::SelGradArgs& a, int B, cudaStream_t st) {
-  constexpr int S = kGradSegment<L>, W = kGradTokens / S;
-  using Tile = sdm::SelGradTile<L, S, W, kGradGroups>;
-  constexpr size_t smem = Tile::kSmemFloats * sizeof(float);
-  set_smem(reinterpret_cast<const void*>(sdm::k_selective_scan_backward<T, L, S, W, kGradGroups>), smem);
-  const dim3 grid(static_cast<unsigned>(p.tiles_per_group) * a.f.G, 1, B);
-  sdm::k_selective_scan_backward<T, L, S, W, kGradGroups><<<grid, Tile::kThreads, smem, st>>>(a);
+template <typename T, int KS, int L>
+sdm_status_t launch_grad_lanes(const sdm::SelGradArgs& a, int B, cudaStream_t st) {
+  constexpr int NG = KS * L / 4;
+  const dim3 grid(static_cast<unsigned>(a.f.tiles_per_group) * a.f.G, a.f.splits, B);
+  sdm::k_selective_scan_grad_maps<T, KS, L><<<grid, sdm::kSelThreads, 0, st>>>(a);
+  sdm_status_t r;
+  if ((r = launch_status("selective_scan_backward maps launch")) != SDM_OK) return r;
+  sdm::k_selective_scan_grad_chain<<<dim3(static_cast<unsigned>(ceil_div(a.f.D, 128)), NG, B), 128, 0, st>>>(a, NG);
+  if ((r = launch_status("selective_scan_backward chain launch")) != SDM_OK) return r;
+  constexpr size_t smem = sizeof(sdm::GradSmem<KS, L>);
+  set_smem(reinterpret_cast<const void*>(sdm::k_selective_scan_grad<T, KS, L>), smem);
+  sdm::k_selective_scan_grad<T, KS, L><<<grid, sdm::kSelThreads, smem, st>>>(a);
   return launch_status("selective_scan_backward launch");
 }
 
 template <typename T>
-sdm_status_t launch_grad(int L, const SelGradPlan& p, const sdm::SelGradArgs& a, int B, cudaStream_t st) {
-  switch (L) {
-    case 2: return launch_grad_lanes<T, 2>(p, a, B, st);
-    case 4: return launch_grad_lanes<T, 4>(p, a, B, st);
-    case 8: return launch_grad_lanes<T, 8>(p, a, B, st);
-    default: return launch_grad_lanes<T, 16>(p, a, B, st);
-  }
+sdm_status_t launch_grad(const sdm::SelGradArgs& a, int B, cudaStream_t st) {
+  if (a.f.N <= 8) return launch_grad_lanes<T, 8, 1>(a, B, st);
+  if (a.f.N <= 16) return launch_grad_lanes<T, 16, 1>(a, B, st);
+  if (a.f.N <= 32) return launch_grad_lanes<T, 16, 2>(a, B, st);
+  return launch_grad_lanes<T, 16, 4>(a, B, st);
 }
 
 sdm_status_t cleared(void* p, size_t n, cudaStream_t st) {
@@ -115,7 +115,6 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
     return ok();
   }
   const SelGradPlan p = sel_grad_plan(s);
-  if (p.tiles > 65535) return fail(SDM_ERR_UNSUPPORTED, "T above 65535 * 64 tokens");
   if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
   if (workspace_bytes < p.total())
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_selective_scan_backward_workspace_bytes");
@@ -124,34 +123,33 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   sdm::SelGradArgs a{};
   a.f = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths, dev->err);
   a.f.tiles_per_group = p.tiles_per_group;
+  a.f.splits = p.splits;
+  a.f.tokens_per_split = p.tokens_per_split;
+  a.tiles = p.tiles;
   char* ws = static_cast<char*>(workspace);
   auto take = [&](size_t n) {
     float* q = reinterpret_cast<float*>(ws);
     ws += n;
     return q;
   };
-  float* ckpt = take(p.ckpt);
+  a.P = reinterpret_cast<float4*>(take(p.split_states));
+  a.H = reinterpret_cast<float4*>(take(p.split_states));
+  a.R = reinterpret_cast<float4*>(take(p.split_states));
+  a.kept = reinterpret_cast<float4*>(take(p.kept));
+  a.sums = take(p.sums);
   a.part_B = take(p.part_bc);
   a.part_C = take(p.part_bc);
-  a.part_A = take(p.part_A);
+  a.part_A = reinterpret_cast<float4*>(take(p.part_A));
   a.part_D = take(p.part_D);
-  a.part_bias = take(p.part_D);
+  a.h0 = h0;
   a.dy = dy;
   a.dstate = dhT;
   a.dx = dx;
   a.ddt = ddt;
   a.dz = dz;
   a.dstate0 = dh0;
-  // States before the tiles: the forward's maps over splits of one tile each.
-  sdm::SelScanArgs f = a.f;
-  f.tiles_per_group = static_cast<int>(ceil_div(s.D / s.G, sel_channels(s.N)));
-  f.splits = p.tiles;
-  f.tokens_per_split = kGradTokens;
-  if ((r = launch_sel_states(s.in_dtype, f, s.B, h0, ckpt, st)) != SDM_OK) return r;
-  a.ckpt = ckpt + static_cast<int64_t>(s.B) * p.tiles * s.D * s.N;
-  const int L = grad_lanes(s.N);
   const bool bf = s.in_dtype == SDM_BF16;
-  if ((r = bf ? launch_grad<bf16>(L, p, a, s.B, st) : launch_grad<float>(L, p, a, s.B, st)) != SDM_OK) return r;
+  if ((r = bf ? launch_grad<bf16>(a, s.B, st) : launch_grad<float>(a, s.B, st)) != SDM_OK) return r;
   const int64_t n = static_cast<int64_t>(s.B) * s.T * s.G * s.N;
   const dim3 grid(static_cast<unsigned>(ceil_div(n, 1024)), 2);
   if (bf)
@@ -161,13 +159,9 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
     sdm::k_selective_scan_sums<float><<<grid, 256, 0, st>>>(a.part_B, a.part_C, p.tiles_per_group, n,
                                                             static_cast<float*>(dB), static_cast<float*>(dC));
   if ((r = launch_status("selective_scan_backward sums launch")) != SDM_OK) return r;
-  auto batch_sum = [&](const float* part, int64_t m, float* out) {
-    if (out == nullptr) return;
-    sdm::k_selective_scan_batch_sum<<<static_cast<unsigned>(ceil_div(m, 256)), 256, 0, st>>>(part, s.B, m, out);
-  };
-  batch_sum(a.part_A, static_cast<int64_t>(s.D) * s.N, dA);
-  batch_sum(a.part_D, s.D, dD);
-  batch_sum(a.part_bias, s.D, ddt_bias);
+  const int NG = p.NP / 4;
+  sdm::k_selective_scan_grad_params<<<dim3(static_cast<unsigned>(ceil_div(s.D, 32)), NG + 1), dim3(32, 8), 0, st>>>(
+      a, NG, s.B * p.splits, dA, dD, ddt_bias);
   if ((r = launch_status("selective_scan_backward parameter sums launch")) != SDM_OK) return r;
   return ok();
 }
