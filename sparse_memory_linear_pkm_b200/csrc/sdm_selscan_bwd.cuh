@@ -21,7 +21,7 @@
 // So every exponential is made three times and nothing else is: that, the
 // exchanges of the sums over channels and the issue slots are about equally
 // loaded. (Four states a lane with segments over warps: 1223 us instead of
-// @@GRAD@@ for B = 2, T = 4096, D = 2048, N = 16 in bf16.)
+// 505 for B = 2, T = 4096, D = 2048, N = 16 in bf16.)
 //
 // The sums over channels (dB, dC) are taken over a warp by halving exchanges,
 // over a block's warps in shared memory, and over blocks by k_selective_scan_sums
@@ -340,7 +340,7 @@ struct GradSmem {
 };
 
 template <typename T, int KS, int L>
-__global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad(const SelGradArgs ga) {
+__global__ void __launch_bounds__(kSelThreads, 3) k_selective_scan_grad(const SelGradArgs ga) {
   using Smem = GradSmem<KS, L>;
   using Sum = ChannelSum<KS, L>;
   constexpr int NP = KS * L, KP = KS / 2, NG = NP / 4, GL = KS / 4;
@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad(const SelGr
     float x[kGradTile], d[kGradTile], e[kGradTile], zg[kGradTile];  // zg: dy silu'(z)
 #pragma unroll
     for (int i = 0; i < kGradTile; i += 2) {
-      const bool on0 = t0 + i < p.t_end, on1 = t0 + i + 1 < p.t_end;
+      // (a lane without a channel adds nothing to the sums over them)
+      const bool on0 = p.live && t0 + i < p.t_end, on1 = p.live && t0 + i + 1 < p.t_end;
       const float2 u = make_float2(rows.d[i].get() + bias, rows.d[i + 1].get() + bias);
       const float2 step = a.softplus ? softplus2(u) : u;
       // sigmoid(u) = exp(u - softplus(u))
@@ -466,10 +467,6 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad(const SelGr
         v[2 * j] = mul2(ee, h[2 * j]);
         v[2 * j + 1] = mul2(ee, h[2 * j + 1]);
       }
-      if (!p.live) {
-#pragma unroll
-        for (int k = 0; k < KP; ++k) v[k] = both(0.f);
-      }
       Sum::run(v);
       if (Sum::writes(lane)) {
         s.sum[buf][1][warp][i][n_sum] = v[0].x;
@@ -504,10 +501,6 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad(const SelGr
           const float2 t = mul2(dd, A2[m]);
           q[m] = mul2(make_float2(ex2(t.x), ex2(t.y)), g);
         }
-      }
-      if (!p.live) {
-#pragma unroll
-        for (int k = 0; k < KP; ++k) v[k] = both(0.f);
       }
       Sum::run(v);
       if (Sum::writes(lane)) {

@@ -32,7 +32,7 @@ SelPlan sel_plan(const sdm_selscan_shape_t& s) {
   const int64_t warps =
       static_cast<int64_t>(s.B) * s.G * ceil_div(s.D / s.G, sel_channels(s.N)) * (sdm::kSelThreads / 32);
   if (warps >= 6 * kSms) return p;
-  const int64_t splits = std::min<int64_t>(ceil_div(32 * kSms, warps), s.T / kSplitTokens);
+  const int64_t splits = std::min<int64_t>(32 * kSms / warps, s.T / kSplitTokens);
   if (splits < 3) return p;
   const int tile = sdm::kSelTile;
   p.tokens_per_split = static_cast<int>(ceil_div(ceil_div(s.T, splits), tile) * tile);

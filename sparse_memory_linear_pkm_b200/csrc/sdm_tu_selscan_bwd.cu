@@ -16,8 +16,9 @@ struct SelGradPlan {
   size_t total() const { return 3 * split_states + kept + sums + 2 * part_bc + part_A + part_D; }
 };
 
-// The token axis is split until 24 warps a SM are there (a split's maps and its
-// start state cost the bandwidth of some 20 tokens), into whole tiles.
+// The token axis is split, into whole tiles, as long as that leaves at most 24
+// warps an SM: two or three whole waves of blocks. (A split's maps and start
+// state cost the bandwidth of some 20 tokens.)
 SelGradPlan sel_grad_plan(const sdm_selscan_shape_t& s) {
   SelGradPlan p;
   p.NP = s.N <= 8 ? 8 : (s.N <= 16 ? 16 : (s.N <= 32 ? 32 : 64));
@@ -25,7 +26,7 @@ SelGradPlan sel_grad_plan(const sdm_selscan_shape_t& s) {
   p.tiles = static_cast<int>(ceil_div(s.T, sdm::kGradTile));
   const int64_t warps = static_cast<int64_t>(s.B) * s.G * p.tiles_per_group * (sdm::kSelThreads / 32);
   const int64_t splits =
-      std::max<int64_t>(1, std::min<int64_t>(ceil_div(24 * kSms, warps), s.T / kGradSplitTokens));
+      std::max<int64_t>(1, std::min<int64_t>(24 * kSms / warps, s.T / kGradSplitTokens));
   p.tokens_per_split = static_cast<int>(ceil_div(ceil_div(s.T, splits), sdm::kGradTile) * sdm::kGradTile);
   p.splits = static_cast<int>(ceil_div(s.T, p.tokens_per_split));
   const size_t f = sizeof(float), row = static_cast<size_t>(s.D) * p.NP * f;
