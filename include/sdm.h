@@ -524,7 +524,8 @@ SDM_API sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtyp
  *   lengths [B] int32 or NULL: tokens of each row; y of later tokens is left as
  *          it was and their x is not read. Values outside [0, T] are clamped
  *          and set the device error word.
- *   y      [B,T,D] in_dtype; must not overlap x. */
+ *   y      [B,T,D] in_dtype; y and state must not overlap x or one another
+ *          (refused). */
 SDM_API sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, const void* w, const void* bias,
                             int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K, int32_t silu, void* state,
                             const int32_t* lengths, void* y, void* stream);
@@ -535,7 +536,8 @@ SDM_API size_t sdm_short_conv_backward_workspace_bytes(int32_t B, int32_t T, int
 /* Gradient of sdm_short_conv for dy = dL/dy and dstate = dL/d(final state)
  * (NULL: none); state0 is the state that the forward started from (NULL: zeros).
  *   dx [B,T,D] in_dtype (0 for tokens past a row's length); dw [D,K] fp32;
- *   dbias [D] fp32 or NULL; dstate0 [B,K-1,D] in_dtype or NULL. Deterministic. */
+ *   dbias [D] fp32 or NULL; dstate0 [B,K-1,D] in_dtype or NULL; dx and dstate0
+ *   must not overlap an input (refused). Deterministic. */
 SDM_API sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in_dtype, const void* w,
                                      const void* bias, int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K,
                                      int32_t silu, const void* state0, const int32_t* lengths, const void* dy,
@@ -570,7 +572,8 @@ SDM_API size_t sdm_selective_scan_workspace_bytes(const sdm_selscan_shape_t* sha
  *   h0 [B,D,N] fp32 or NULL (zeros): the state before the first token;
  *   hT [B,D,N] fp32 or NULL: the state after each row's last token; may be h0,
  *     so that consecutive calls continue one sequence (T = 1 to decode)
- *   y [B,T,D] in_dtype; must not overlap the inputs. */
+ *   y [B,T,D] in_dtype. y and hT must not overlap an input or one another, but
+ *     for hT == h0 (refused). */
 SDM_API sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x, const void* dt, const float* A,
                                 const void* Bm, const void* Cm, const float* Dskip, const void* z,
                                 const float* dt_bias, const int32_t* lengths, const float* h0, float* hT, void* y,
@@ -580,12 +583,12 @@ SDM_API sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const 
 SDM_API size_t sdm_selective_scan_backward_workspace_bytes(const sdm_selscan_shape_t* shape);
 
 /* Gradient of sdm_selective_scan for dy = dL/dy and dhT = dL/dhT (NULL: none).
- * The states are computed again from h0 (checkpoints every 64 tokens in the
- * workspace).
+ * The states are computed again from h0 (states before every fourth token in
+ * the workspace).
  *   dx, ddt, dz (with z) [B,T,D], dB, dC [B,T,G,N]: in_dtype, contiguous, 0 for
  *   tokens past a row's length; dA [D,N], dD [D], ddt_bias [D] fp32 (the last
- *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL.
- * Deterministic. */
+ *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL. Outputs
+ *   must not overlap inputs. Deterministic. */
 SDM_API sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const void* x, const void* dt,
                                          const float* A, const void* Bm, const void* Cm, const float* Dskip,
                                          const void* z, const float* dt_bias, const int32_t* lengths,
@@ -611,8 +614,9 @@ SDM_API size_t sdm_grad_norm_clip_workspace_bytes(int32_t n_tensors);
  * tensors is a HOST array, read during the call. norm: one fp32 on the device.
  * max_norm may be infinite (out_i = grad_i). Squares beyond fp32's range are
  * summed in 64 bits; a norm that is not finite gives c = 0 or not a number, as
- * the formula does. Outputs must not overlap other tensors. The sums have a
- * fixed order. */
+ * the formula does. An output that shares memory with another tensor of the list
+ * (the same tensor twice, in place) or with part of its own gradient is refused.
+ * The sums have a fixed order. */
 SDM_API sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tensors, float max_norm, float eps,
                                 float* norm, void* workspace, size_t workspace_bytes, void* stream);
 

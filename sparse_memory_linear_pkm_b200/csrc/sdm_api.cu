@@ -139,6 +139,18 @@ sdm_status_t need_ptr(const void* p, const char* name, bool nonempty) {
   return SDM_OK;
 }
 
+sdm_status_t check_apart(const Piece* outs, int n_outs, const Piece* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i], ins[j]))
+        return fail(SDM_ERR_INVALID_ARGUMENT, std::string(outs[i].name) + " overlaps " + ins[j].name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j]))
+        return fail(SDM_ERR_INVALID_ARGUMENT, std::string(outs[i].name) + " overlaps " + outs[j].name);
+  }
+  return SDM_OK;
+}
+
 size_t in_size(int32_t d) { return d == SDM_BF16 ? 2 : 4; }
 size_t state_size(int32_t d) { return d == SDM_FP8_B16 ? 1 : in_size(d); }
 

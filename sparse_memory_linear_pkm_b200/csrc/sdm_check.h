@@ -41,4 +41,17 @@ bool aligned16(const void* p);
 size_t in_size(int32_t dtype);
 size_t align256(size_t x);
 
+// A piece of memory by name, and whether two of them share a byte.
+struct Piece {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+inline bool overlap(const Piece& a, const Piece& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p != nullptr && b.p != nullptr && x < y + b.bytes && y < x + a.bytes;
+}
+// SDM_ERR_INVALID_ARGUMENT if an output shares a byte with an input or another output.
+sdm_status_t check_apart(const Piece* outs, int n_outs, const Piece* ins, int n_ins);
+
 }  // namespace sdm_host

@@ -24,10 +24,16 @@ inline int sel_channels(int32_t N) { return sdm::kSelThreads / sel_lanes(N); }
 sdm_status_t check_selscan(const sdm_selscan_shape_t* s);
 sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const void* dt, const float* A,
                               const void* Bm, const void* Cm, const float* Dskip, const void* z,
-                              const float* dt_bias, const int32_t* lengths, unsigned* err);
+                              const float* dt_bias, const int32_t* lengths);
 sdm_status_t need_selscan(const sdm_selscan_shape_t& s, bool any, const void* x, const void* dt, const float* A,
                           const void* Bm, const void* Cm, const float* Dskip, const void* z, const float* dt_bias,
                           const int32_t* lengths);
+
+// The memory that a call's token inputs take, for check_apart: x, dt, z, B, C.
+struct SelInputs {
+  Piece piece[5];
+};
+SelInputs selscan_inputs(const sdm_selscan_shape_t& s, const sdm::SelScanArgs& a);
 
 // The scan over a.splits parts of the token axis, from the states in a.h_in.
 sdm_status_t launch_sel_run(int32_t in_dtype, const sdm::SelScanArgs& a, int B, cudaStream_t st);

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <vector>
 
 #include "sdm_check.h"
 #include "sdm_clip.cuh"
@@ -39,6 +40,63 @@ sdm_status_t check_tensor(const sdm_grad_tensor_t& t, int i) {
     return bad(SDM_ERR_INVALID_ARGUMENT, ".out is not aligned to its element size");
   if (t.out == t.grad && t.out_dtype != t.dtype)
     return bad(SDM_ERR_INVALID_ARGUMENT, " is its own output in another type");
+  return SDM_OK;
+}
+
+// Outputs must not share a byte with another tensor, whichever of the two the
+// list names first: the second pass reads and writes in any order. A sweep over
+// all pieces by address, with the two furthest ends of pieces so far that belong
+// to different tensors (one is always another's), of all pieces and of outputs.
+sdm_status_t check_outputs_apart(const sdm_grad_tensor_t* t, int n) {
+  struct Span {
+    uintptr_t begin, end;
+    int of;
+    bool out;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * static_cast<size_t>(n));
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = reinterpret_cast<uintptr_t>(t[i].out);
+    if (g != o) spans.push_back({g, g + t[i].n * in_size(t[i].dtype), i, false});
+    if (o != 0) spans.push_back({o, o + t[i].n * in_size(t[i].out_dtype), i, true});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  struct Ends {
+    uintptr_t end[2] = {0, 0};
+    int of[2] = {-1, -1};
+    void add(uintptr_t e, int i) {
+      if (i == of[0]) {
+        end[0] = std::max(end[0], e);
+      } else if (e > end[0]) {
+        end[1] = end[0];
+        of[1] = of[0];
+        end[0] = e;
+        of[0] = i;
+      } else if (e > end[1]) {
+        end[1] = e;
+        of[1] = i;
+      }
+    }
+    int other(uintptr_t begin, int i) const {  // a different tensor that reaches past `begin`, or -1
+      const int k = of[0] == i ? 1 : 0;
+      return of[k] >= 0 && end[k] > begin ? of[k] : -1;
+    }
+  } any, outs;
+  for (const Span& s : spans) {
+    const int hit = (s.out ? any : outs).other(s.begin, s.of);
+    if (hit >= 0)
+      return fail(SDM_ERR_INVALID_ARGUMENT, "tensors[" + std::to_string(std::max(hit, s.of)) + "] and tensors[" +
+                                                std::to_string(std::min(hit, s.of)) + "] overlap in an output");
+    // A tensor's own output may be its gradient's memory, but not part of it.
+    if (s.out && t[s.of].out != t[s.of].grad) {
+      const uintptr_t g = reinterpret_cast<uintptr_t>(t[s.of].grad);
+      if (g < s.end && s.begin < g + t[s.of].n * in_size(t[s.of].dtype))
+        return fail(SDM_ERR_INVALID_ARGUMENT, "tensors[" + std::to_string(s.of) + "].out overlaps its own grad");
+    }
+    any.add(s.end, s.of);
+    if (s.out) outs.add(s.end, s.of);
+  }
   return SDM_OK;
 }
 
@@ -103,6 +161,7 @@ sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tens
     if ((r = check_tensor(t, i)) != SDM_OK) return r;
     write |= t.out != nullptr && t.n > 0;
   }
+  if (write && (r = check_outputs_apart(tensors, n_tensors)) != SDM_OK) return r;
   if ((r = need_gate(norm, "norm", true, SDM_F32)) != SDM_OK) return r;
   const ClipPlan p = clip_plan(tensors, n_tensors);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

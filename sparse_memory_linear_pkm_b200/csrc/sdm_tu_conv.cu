@@ -41,12 +41,6 @@ bool whole_taps(const void* w, int32_t dtype, int32_t K) {
   return K == 4 && reinterpret_cast<uintptr_t>(w) % (4 * in_size(dtype)) == 0;
 }
 
-// Whether two arrays of these sizes share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
-}
-
 template <typename T, int KT>
 void launch_conv_taps(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(ceil_div(a.per_seq, 256)), B);
@@ -111,8 +105,11 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
   const int64_t stride = x_stride == 0 ? D : x_stride;
   const size_t es = in_size(in_dtype);
   const int64_t tokens = static_cast<int64_t>(B) * T;
-  if (overlap(x, (static_cast<size_t>(tokens - 1) * stride + D) * es, y, static_cast<size_t>(tokens) * D * es))
-    return fail(SDM_ERR_INVALID_ARGUMENT, "y overlaps x (threads read neighbours' inputs)");
+  // (Threads read their neighbours' inputs.)
+  const size_t row = static_cast<size_t>(D) * es, sb = static_cast<size_t>(B) * (K - 1) * row;
+  const Piece ins[] = {{"x", x, (static_cast<size_t>(tokens - 1) * stride) * es + row}};
+  const Piece outs[] = {{"y", y, static_cast<size_t>(tokens) * row}, {"state", state, sb}};
+  if ((r = check_apart(outs, 2, ins, 1)) != SDM_OK) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
   const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvV);
@@ -167,11 +164,14 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_short_conv_backward_workspace_bytes");
   const int64_t stride = x_stride == 0 ? D : x_stride;
   const int64_t tokens = static_cast<int64_t>(B) * T;
-  const size_t nb = static_cast<size_t>(tokens) * D * es;
-  if (overlap(dx, nb, dy, nb) || overlap(dx, nb, x, (static_cast<size_t>(tokens - 1) * stride + D) * es))
-    return fail(SDM_ERR_INVALID_ARGUMENT, "dx overlaps x or dy (threads read neighbours' inputs)");
-  if (dstate0 != nullptr && (dstate0 == dstate || dstate0 == state0))
-    return fail(SDM_ERR_INVALID_ARGUMENT, "dstate0 overlaps state0 or dstate");
+  const size_t row = static_cast<size_t>(D) * es, nb = static_cast<size_t>(tokens) * row;
+  const size_t sb = static_cast<size_t>(B) * (K - 1) * row;
+  const Piece ins[] = {{"x", x, (static_cast<size_t>(tokens - 1) * stride) * es + row},
+                       {"dy", dy, nb},
+                       {"state0", state0, sb},
+                       {"dstate", dstate, sb}};
+  const Piece outs[] = {{"dx", dx, nb}, {"dstate0", dstate0, sb}};
+  if ((r = check_apart(outs, 2, ins, 4)) != SDM_OK) return r;
   if (p.slots > 65535) return fail(SDM_ERR_UNSUPPORTED, "B * T above 65535 * 512 tokens");
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;

@@ -108,7 +108,7 @@ sdm_status_t check_selscan(const sdm_selscan_shape_t* s) {
 // The kernels' view of a call's inputs.
 sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const void* dt, const float* A,
                               const void* Bm, const void* Cm, const float* Dskip, const void* z,
-                              const float* dt_bias, const int32_t* lengths, unsigned* err) {
+                              const float* dt_bias, const int32_t* lengths) {
   sdm::SelScanArgs a{};
   a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.bias = dt_bias;
   a.lengths = lengths;
@@ -122,7 +122,6 @@ sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const
   a.splits = 1;
   a.tokens_per_split = s.T;
   a.softplus = s.softplus != 0;
-  a.err = err;
   // Rows read in units of four: address, stride and each group's first channel
   // (or state) on whole units.
   const size_t unit = 4 * in_size(s.in_dtype);
@@ -133,6 +132,16 @@ sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const
             (z == nullptr || whole(z, a.z_stride));
   a.vec_b = s.N % 4 == 0 && whole(Bm, a.b_stride) && whole(Cm, a.c_stride);
   return a;
+}
+
+SelInputs selscan_inputs(const sdm_selscan_shape_t& s, const sdm::SelScanArgs& a) {
+  const size_t es = in_size(s.in_dtype), last = static_cast<size_t>(s.B) * s.T - 1;
+  const size_t gn = static_cast<size_t>(s.G) * s.N, d = s.D;
+  return {{{"x", a.x, (last * a.x_stride + d) * es},
+           {"dt", a.dt, (last * a.dt_stride + d) * es},
+           {"z", a.z, (last * a.z_stride + d) * es},
+           {"Bm", a.Bm, (last * a.b_stride + gn) * es},
+           {"Cm", a.Cm, (last * a.c_stride + gn) * es}}};
 }
 
 // The pointers that the scan and its gradient share.
@@ -191,9 +200,15 @@ sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x,
     if (workspace_bytes < 2 * p.state_bytes)
       return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_selective_scan_workspace_bytes");
   }
+  sdm::SelScanArgs a = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths);
+  const SelInputs in = selscan_inputs(s, a);
+  const size_t states = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
+  const Piece outs[] = {{"y", y, static_cast<size_t>(s.B) * s.T * s.D * in_size(s.in_dtype)}, {"hT", hT, states}};
+  const Piece start = {"h0", hT == h0 ? nullptr : h0, states};
+  if ((r = check_apart(outs, 2, in.piece, 5)) || (r = check_apart(outs, 2, &start, 1))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  sdm::SelScanArgs a = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths, dev->err);
+  a.err = dev->err;
   a.h_in = h0;
   a.h_out = hT;
   a.y = y;

@@ -119,10 +119,18 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
   if (workspace_bytes < p.total())
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_selective_scan_backward_workspace_bytes");
+  sdm::SelGradArgs a{};
+  a.f = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths);
+  const SelInputs in = selscan_inputs(s, a.f);
+  const size_t es = in_size(s.in_dtype), tokens = static_cast<size_t>(s.B) * s.T, rows = tokens * s.D * es;
+  const size_t bc = tokens * s.G * s.N * es;
+  const Piece more[] = {{"dy", dy, rows}, {"h0", h0, states}};
+  const Piece outs[] = {{"dx", dx, rows}, {"ddt", ddt, rows}, {"dz", dz, rows}, {"dB", dB, bc},
+                        {"dC", dC, bc},   {"dA", dA, static_cast<size_t>(s.D) * s.N * sizeof(float)}};
+  if ((r = check_apart(outs, 6, in.piece, 5)) || (r = check_apart(outs, 6, more, 2))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  sdm::SelGradArgs a{};
-  a.f = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths, dev->err);
+  a.f.err = dev->err;
   a.f.tiles_per_group = p.tiles_per_group;
   a.f.splits = p.splits;
   a.f.tokens_per_split = p.tokens_per_split;

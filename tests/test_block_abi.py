@@ -85,7 +85,8 @@ def conv_args(**kw):
     (dict(y=None), "y is NULL", 1), (dict(y=ctypes.c_void_p((1 << 24) + 2)), "y is not 16-byte", 1),
     (dict(K=1), "K must", 1), (dict(K=9), "K must", 1), (dict(B=-1), "B, T and D", 1), (dict(B=65536), "B above", 2),
     (dict(x_stride=23), "x_stride", 1), (dict(in_dtype=2), "in_dtype", 1), (dict(w_dtype=2), "w_dtype", 1),
-    (dict(T=2 ** 31 - 1, D=24), "above 2^31", 2), (dict(y=P), "y overlaps x", 1)])
+    (dict(T=2 ** 31 - 1, D=24), "above 2^31", 2), (dict(y=P), "y overlaps x", 1),
+    (dict(state=ctypes.c_void_p((1 << 24) + 16)), "state overlaps y", 1), (dict(state=P), "state overlaps x", 1)])
 def test_conv_refuses(lib, kw, text, code):
     refused(lib, lib.sdm_short_conv(*conv_args(**kw)), text, code)
 
@@ -143,6 +144,15 @@ def test_scan_refuses_pointers(lib):
         if n in ("x", "dt", "A", "Bm", "Cm", "y"):
             args[i] = None
             refused(lib, lib.sdm_selective_scan(s, *args, None, 0, None), n + " is NULL")
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(12)]
+    for i, text in ((11, "y overlaps"), (10, "hT overlaps")):
+        for j in (0, 1, 3, 4, 6):
+            args = list(far)
+            args[i] = ctypes.c_void_p(far[j].value + 16)
+            refused(lib, lib.sdm_selective_scan(s, *args, None, 0, None), f"{text} {names[j]}")
+    args = list(far)
+    args[10] = ctypes.c_void_p(far[9].value + 64)
+    refused(lib, lib.sdm_selective_scan(s, *args, None, 0, None), "hT overlaps h0")
     assert lib.sdm_selective_scan(None, *([P] * 13), 0, None) == 1
     for kw in (dict(B=0), dict(D=0)):
         assert lib.sdm_selective_scan(ctypes.byref(shape(**kw)), *([None] * 13), 0, None) == 0
@@ -169,6 +179,11 @@ def test_scan_gradient_refuses(lib):
             args[i] = None
             refused(lib, lib.sdm_selective_scan_backward(ctypes.byref(s), *args, need, None), n + " is NULL")
     refused(lib, lib.sdm_selective_scan_backward(ctypes.byref(s), *([P] * 22), need - 1, None), "workspace is smaller")
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(22)]
+    for i, j in ((12, 0), (13, 10), (18, 6), (15, 3), (16, 15), (14, 1)):
+        args = list(far)
+        args[i] = far[j]
+        refused(lib, lib.sdm_selective_scan_backward(ctypes.byref(s), *args, need, None), f"{names[i]} overlaps {names[j]}")
 
 
 def clip(lib, entries, max_norm=1.0, eps=1e-6, norm=P, ws=P, ws_bytes=None):
@@ -186,6 +201,12 @@ def test_clip_refuses(lib):
                         ((a, a, 5, native.BF16, native.F32), "its own output")):
         refused(lib, clip(lib, [good, entry]), text)
     refused(lib, clip(lib, [(a, o, 2 ** 41, 0, 0)]), "2^40", 2)
+    # the same tensor twice, outputs that overlap, an output on another's gradient, or inside its own
+    for first, second in (((a, a, 100, 0, 0), (a, a, 100, 0, 0)), (good, (a + 4096, o + 396, 5, 0, 0)),
+                          (good, (o + 200, 1 << 26, 10, 0, 0)), ((o + 200, 1 << 26, 10, 0, 0), good),
+                          ((a, a, 1000, 0, 0), (a + 16, o, 4, 0, 0))):
+        refused(lib, clip(lib, [first, (1 << 27, 1 << 28, 7, 1, 0), second]), "overlap in an output")
+    refused(lib, clip(lib, [(a, a + 4, 100, 0, 0)]), "out overlaps its own grad")
     refused(lib, clip(lib, [good], max_norm=-1.0), "max_norm")
     refused(lib, clip(lib, [good], max_norm=float("nan")), "max_norm")
     refused(lib, clip(lib, [good], eps=-1.0), "eps")
