@@ -111,17 +111,16 @@ __device__ __forceinline__ void conv_store(T* p, int n, const float2* o) {
   }
 }
 
-constexpr int kConvV = 4;      // channels of a forward thread
 constexpr int kConvAhead = 4;  // tokens loaded together, one such run before they are used
 static_assert(kConvMaxK - 1 <= 2 * kConvAhead, "runs are at least two of these, so only the first reaches the state");
 
-// A thread walks one run of tokens of kConvV channels with the last KT - 1
-// inputs in registers. The thread of a sequence's first run also moves the
+// A thread walks one run of tokens of V channels with the last KT - 1 inputs in
+// registers. The thread of a sequence's first run also moves the
 // state: it alone reads the old one, and the new one comes from x and the old
 // one, so both may be one buffer.
-template <typename T, int KT, bool kVec>
+template <typename T, int KT, int V, bool kVec>
 __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
-  constexpr int V = kConvV, P = V / 2;
+  constexpr int P = V / 2;
   const unsigned id = blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= a.per_seq) return;
   const int run = static_cast<int>(id / static_cast<unsigned>(a.units));

@@ -40,46 +40,42 @@ struct NormArgs {
   float eps;
 };
 
-// The columns of a row that a thread owns: kNormV vectors of 8 consecutive
-// values (kVec), or single values tpr apart (rows that are not whole 16-byte
-// units).
-template <bool kVec>
-__device__ __forceinline__ int norm_col(int j, int i, int t, int tpr) {
-  return kVec ? (j * tpr + t) * 8 + i : (j * 8 + i) * tpr + t;
+// The columns of a row that a thread owns: 8 values a vector, in units of kW
+// neighbours (8, 4, 2 or 1, the widest that rows of d values are whole units
+// of); the units of the row's threads follow one another.
+template <int kW>
+__device__ __forceinline__ int norm_col(int j, int u, int t, int tpr) {  // first column of unit u of vector j
+  return ((j * (8 / kW) + u) * tpr + t) * kW;
 }
 
-template <typename T, bool kVec>
+template <typename T, int kW>
 __device__ __forceinline__ void norm_load(const T* row, int j, int t, int tpr, int d, float2* pairs) {
   float v[8];
-  if (kVec) {
-    if (norm_col<true>(j, 0, t, tpr) < d) {
-      load8<T>(row + norm_col<true>(j, 0, t, tpr), v);
+#pragma unroll
+  for (int u = 0; u < 8 / kW; ++u) {
+    const int c = norm_col<kW>(j, u, t, tpr);
+    if (c < d) {
+      if constexpr (kW == 8) load8<T>(row + c, v);
+      else load_unit<T, kW>(row + c, v + u * kW);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = norm_col<false>(j, i, t, tpr);
-      v[i] = c < d ? to_f32<T>(row[c]) : 0.f;
+      for (int i = 0; i < kW; ++i) v[u * kW + i] = 0.f;
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) pairs[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
-template <typename T, bool kVec>
+template <typename T, int kW>
 __device__ __forceinline__ void norm_store(T* row, int j, int t, int tpr, int d, const float2* pairs) {
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[2 * i] = pairs[i].x, v[2 * i + 1] = pairs[i].y;
-  if (kVec) {
-    if (norm_col<true>(j, 0, t, tpr) < d) store8<T>(row + norm_col<true>(j, 0, t, tpr), v);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = norm_col<false>(j, i, t, tpr);
-      if (c < d) row[c] = from_f32<T>(v[i]);
+  for (int u = 0; u < 8 / kW; ++u) {
+    const int c = norm_col<kW>(j, u, t, tpr);
+    if (c < d) {
+      if constexpr (kW == 8) store8<T>(row + c, v);
+      else store_unit<T, kW>(row + c, v + u * kW);
     }
   }
 }
@@ -248,7 +244,7 @@ __device__ __forceinline__ double quotient64(double s, float c) {
   return s * r;
 }
 
-template <typename Tx, typename Tr, int kOut, bool kBlock, bool kVec>
+template <typename Tx, typename Tr, int kOut, bool kBlock, int kW>
 __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8)
     k_rmsnorm_residual(const NormArgs a) {
   constexpr bool k8bit = kOut >= kNormFp8Blk;
@@ -261,8 +257,8 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
   float2 w[kNormV][4];
 #pragma unroll
   for (int j = 0; j < kNormV; ++j) {
-    if (a.w_bf16) norm_load<bf16, kVec>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
-    else norm_load<float, kVec>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
+    if (a.w_bf16) norm_load<bf16, kW>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
+    else norm_load<float, kW>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
   }
   if (kOut == kNormFp8Row && kBlock && threadIdx.x == 0) s_max[0] = 0ull;
   int turn = 0;
@@ -273,11 +269,11 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
     const int64_t at = (live ? row : 0) * d;
     float2 h[kNormV][4];
 #pragma unroll
-    for (int j = 0; j < kNormV; ++j) norm_load<Tx, kVec>(static_cast<const Tx*>(a.x) + at, j, t, tpr, d, h[j]);
+    for (int j = 0; j < kNormV; ++j) norm_load<Tx, kW>(static_cast<const Tx*>(a.x) + at, j, t, tpr, d, h[j]);
     if (a.r != nullptr) {
       float2 r[kNormV][4];
 #pragma unroll
-      for (int j = 0; j < kNormV; ++j) norm_load<Tr, kVec>(static_cast<const Tr*>(a.r) + at, j, t, tpr, d, r[j]);
+      for (int j = 0; j < kNormV; ++j) norm_load<Tr, kW>(static_cast<const Tr*>(a.r) + at, j, t, tpr, d, r[j]);
 #pragma unroll
       for (int j = 0; j < kNormV; ++j) {
 #pragma unroll
@@ -285,7 +281,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
           h[j][i] = add2(h[j][i], r[j][i]);
           h[j][i] = make_float2(round_to<Tr>(h[j][i].x), round_to<Tr>(h[j][i].y));
         }
-        if (live) norm_store<Tr, kVec>(static_cast<Tr*>(a.h) + at, j, t, tpr, d, h[j]);
+        if (live) norm_store<Tr, kW>(static_cast<Tr*>(a.h) + at, j, t, tpr, d, h[j]);
       }
     }
     if constexpr (!k8bit) {
@@ -301,7 +297,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
       for (int j = 0; j < kNormV; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[j][i] = mul2(mul2(h[j][i], both(s)), w[j][i]);
-        if (live) norm_store<Ty, kVec>(static_cast<Ty*>(a.y) + at, j, t, tpr, d, h[j]);
+        if (live) norm_store<Ty, kW>(static_cast<Ty*>(a.y) + at, j, t, tpr, d, h[j]);
       }
     } else {
       SumMax v{0.0, 0.f};
@@ -325,7 +321,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
         int8_t* exps = static_cast<int8_t*>(a.scales) + at / 16;
 #pragma unroll
         for (int j = 0; j < kNormV; ++j) {
-          const int c = norm_col<true>(j, 0, t, tpr);
+          const int c = norm_col<8>(j, 0, t, tpr);
           int e;
           const uint2 q = norm_fp8blk(h[j], w[j], s, live && c < d, &e);
           if (live && c < d) {
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
         const bool range = kf > 1e-30f && kf < 1e30f && v.max < 1e30f;
 #pragma unroll
         for (int j = 0; j < kNormV; ++j) {
-          const int c = norm_col<true>(j, 0, t, tpr);
+          const int c = norm_col<8>(j, 0, t, tpr);
           float2 u[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) u[i] = mul2(mul2(h[j][i], w[j][i]), both(kf));
@@ -428,7 +424,7 @@ struct NormGradArgs {
 // rows it meets in registers and writes them to its row group's slot, so dw is
 // the same on every run (k_sum_slots adds the slots in a fixed order).
 // All of a row's loads go out before the first sum.
-template <typename T, typename Tdy, bool kBlock, bool kVec>
+template <typename T, typename Tdy, bool kBlock, int kW>
 __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_residual_backward(const NormGradArgs a) {
   __shared__ float2 buf[2][32];
   const int d = a.d, tpr = a.tpr;
@@ -438,8 +434,8 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
   float2 w[kNormV][4], acc[kNormV][4];
 #pragma unroll
   for (int j = 0; j < kNormV; ++j) {
-    if (a.w_bf16) norm_load<bf16, kVec>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
-    else norm_load<float, kVec>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
+    if (a.w_bf16) norm_load<bf16, kW>(static_cast<const bf16*>(a.w), j, t, tpr, d, w[j]);
+    else norm_load<float, kW>(static_cast<const float*>(a.w), j, t, tpr, d, w[j]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
   }
@@ -452,10 +448,10 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
     float2 h[kNormV][4], g[kNormV][4], o[kNormV][4];
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) {
-      norm_load<T, kVec>(static_cast<const T*>(a.h) + at, j, t, tpr, d, h[j]);
-      norm_load<Tdy, kVec>(static_cast<const Tdy*>(a.dy) + at, j, t, tpr, d, g[j]);
+      norm_load<T, kW>(static_cast<const T*>(a.h) + at, j, t, tpr, d, h[j]);
+      norm_load<Tdy, kW>(static_cast<const Tdy*>(a.dy) + at, j, t, tpr, d, g[j]);
       if (a.dh != nullptr) {
-        norm_load<T, kVec>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o[j]);
+        norm_load<T, kW>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = both(0.f);
@@ -481,12 +477,12 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
         const float2 own = fma2(h[j][i], both(-corr), mul2(mul2(g[j][i], w[j][i]), both(s)));
         o[j][i] = add2(o[j][i], own);
       }
-      if (live) norm_store<T, kVec>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o[j]);
+      if (live) norm_store<T, kW>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o[j]);
     }
   }
   float* slot = a.part + (static_cast<int64_t>(blockIdx.x) * rpb + group) * d;
 #pragma unroll
-  for (int j = 0; j < kNormV; ++j) norm_store<float, kVec>(slot, j, t, tpr, d, acc[j]);
+  for (int j = 0; j < kNormV; ++j) norm_store<float, kW>(slot, j, t, tpr, d, acc[j]);
 }
 
 // out[c] = sum over slots of part[slot, c], in a fixed order: 32 columns a

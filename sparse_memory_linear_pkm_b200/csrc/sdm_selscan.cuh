@@ -54,7 +54,7 @@ struct SelScanArgs {
   int in_splits;           // h_in holds one state per split ([B, splits, D, N])
   int tokens_per_split;
   int softplus;
-  int vec_x, vec_b;        // rows of channels / of B and C are whole aligned units of four
+  int vec_b;               // rows of B and C are whole aligned units of four states
   unsigned* err;
 };
 
@@ -78,29 +78,7 @@ __device__ __forceinline__ float2 softplus2(float2 u) {
   return fma2(e, q, make_float2(fmaxf(u.x, 0.0f), fmaxf(u.y, 0.0f)));
 }
 
-// V channels of token row p, of which `n` exist; zeros elsewhere.
-template <typename T, int V>
-__device__ __forceinline__ void load_channels(const T* p, bool vec, int n, float* v) {
-  if (vec && n >= V) {
-    load_unit<T, V>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < n ? to_f32<T>(p[i]) : 0.f;
-  }
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_channels(T* p, bool vec, int n, const float* v) {
-  if (vec && n >= V) {
-    store_unit<T, V>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
-  }
-}
-
-// Four states n .. n+3 of an [.., N] fp32 row; zeros past N. `whole`: N % 4 == 0.
+// Four states n .. n+3 of an [.., N] fp32 row; zeros past N.
 __device__ __forceinline__ void load_states(const float* row, int n, int N, float* v) {
   if (N % 4 == 0) {
     if (n < N) {

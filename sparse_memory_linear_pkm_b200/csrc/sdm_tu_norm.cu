@@ -15,13 +15,14 @@ namespace {
 // Threads per row and block size. A row of up to 512 values takes a power-of-two
 // part of a warp (several rows a block, no block barrier); a longer one a block.
 struct NormPlan {
-  bool block, vec;
+  bool block;
+  int width;  // neighbouring values of a memory access: the widest that rows are whole units of
   int tpr, threads, rpb;
 };
 NormPlan norm_plan(int32_t d) {
   NormPlan p;
   const int need = (d + 8 * sdm::kNormV - 1) / (8 * sdm::kNormV);
-  p.vec = d % 8 == 0;
+  p.width = d % 8 == 0 ? 8 : (d % 4 == 0 ? 4 : (d % 2 == 0 ? 2 : 1));
   p.block = need > 32;
   if (p.block) {
     p.tpr = (need + 31) / 32 * 32;
@@ -55,14 +56,20 @@ sdm_status_t check_norm(int64_t n_rows, int32_t d, float eps) {
   return SDM_OK;
 }
 
+template <typename Tx, typename Tr, int kOut, int kW>
+void launch_norm_width(const NormPlan& p, unsigned grid, const sdm::NormArgs& a, cudaStream_t st) {
+  if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, kW><<<grid, p.threads, 0, st>>>(a);
+  else sdm::k_rmsnorm_residual<Tx, Tr, kOut, false, kW><<<grid, p.threads, 0, st>>>(a);
+}
+
 template <typename Tx, typename Tr, int kOut>
 void launch_norm(const NormPlan& p, unsigned grid, const sdm::NormArgs& a, cudaStream_t st) {
-  if (p.vec) {
-    if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, true><<<grid, p.threads, 0, st>>>(a);
-    else sdm::k_rmsnorm_residual<Tx, Tr, kOut, false, true><<<grid, p.threads, 0, st>>>(a);
+  if (kOut >= sdm::kNormFp8Blk || p.width == 8) {
+    launch_norm_width<Tx, Tr, kOut, 8>(p, grid, a, st);
   } else if constexpr (kOut < sdm::kNormFp8Blk) {
-    if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, false><<<grid, p.threads, 0, st>>>(a);
-    else sdm::k_rmsnorm_residual<Tx, Tr, kOut, false, false><<<grid, p.threads, 0, st>>>(a);
+    if (p.width == 4) launch_norm_width<Tx, Tr, kOut, 4>(p, grid, a, st);
+    else if (p.width == 2) launch_norm_width<Tx, Tr, kOut, 2>(p, grid, a, st);
+    else launch_norm_width<Tx, Tr, kOut, 1>(p, grid, a, st);
   }
 }
 
@@ -76,14 +83,19 @@ void launch_norm_out(int out, const NormPlan& p, unsigned grid, const sdm::NormA
   }
 }
 
+template <typename T, typename Tdy, int kW>
+void launch_norm_grad_width(const NormPlan& p, unsigned grid, const sdm::NormGradArgs& a, cudaStream_t st) {
+  if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, kW><<<grid, p.threads, 0, st>>>(a);
+  else sdm::k_rmsnorm_residual_backward<T, Tdy, false, kW><<<grid, p.threads, 0, st>>>(a);
+}
+
 template <typename T, typename Tdy>
 void launch_norm_grad(const NormPlan& p, unsigned grid, const sdm::NormGradArgs& a, cudaStream_t st) {
-  if (p.vec) {
-    if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, true><<<grid, p.threads, 0, st>>>(a);
-    else sdm::k_rmsnorm_residual_backward<T, Tdy, false, true><<<grid, p.threads, 0, st>>>(a);
-  } else {
-    if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, false><<<grid, p.threads, 0, st>>>(a);
-    else sdm::k_rmsnorm_residual_backward<T, Tdy, false, false><<<grid, p.threads, 0, st>>>(a);
+  switch (p.width) {
+    case 8: launch_norm_grad_width<T, Tdy, 8>(p, grid, a, st); break;
+    case 4: launch_norm_grad_width<T, Tdy, 4>(p, grid, a, st); break;
+    case 2: launch_norm_grad_width<T, Tdy, 2>(p, grid, a, st); break;
+    default: launch_norm_grad_width<T, Tdy, 1>(p, grid, a, st); break;
   }
 }
 

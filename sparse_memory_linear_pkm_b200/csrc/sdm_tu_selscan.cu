@@ -122,14 +122,10 @@ sdm::SelScanArgs selscan_args(const sdm_selscan_shape_t& s, const void* x, const
   a.splits = 1;
   a.tokens_per_split = s.T;
   a.softplus = s.softplus != 0;
-  // Rows read in units of four: address, stride and each group's first channel
-  // (or state) on whole units.
   const size_t unit = 4 * in_size(s.in_dtype);
   auto whole = [&](const void* p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % unit == 0 && stride % 4 == 0;
   };
-  a.vec_x = (s.D / s.G) % 4 == 0 && whole(x, a.x_stride) && whole(dt, a.dt_stride) &&
-            (z == nullptr || whole(z, a.z_stride));
   a.vec_b = s.N % 4 == 0 && whole(Bm, a.b_stride) && whole(Cm, a.c_stride);
   return a;
 }
