@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan_grad_maps(const 
         const float4 Bv = sB[i * NG + k / 2], Cv = sC[i * NG + k / 2];
 #pragma unroll
         for (int m = k; m < k + 2; ++m) {
-          const float2 q = mul2(dd, A2[m]);
-          const float2 at = make_float2(ex2(q.x), ex2(q.y));
+          const float2 at = decay2(dd, A2[m]);
           h[m] = fma2(at, h[m], mul2(w, m == k ? low2(Bv) : high2(Bv)));
           P[m] = mul2(P[m], at);
           R[m] = fma2(P[m], mul2(ee, m == k ? low2(Cv) : high2(Cv)), R[m]);
@@ -457,9 +456,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) k_selective_scan_grad(const Se
 #pragma unroll
       for (int j = 0; j < GL; ++j) {
         const float4 Bv = sB[i * NG + (j ^ order)], Cv = sC[i * NG + (j ^ order)];
-        const float2 p0 = mul2(dd, A2[2 * j]), p1 = mul2(dd, A2[2 * j + 1]);
-        const float2 u0 = mul2(make_float2(ex2(p0.x), ex2(p0.y)), h[2 * j]);
-        const float2 u1 = mul2(make_float2(ex2(p1.x), ex2(p1.y)), h[2 * j + 1]);
+        const float2 u0 = mul2(decay2(dd, A2[2 * j]), h[2 * j]);
+        const float2 u1 = mul2(decay2(dd, A2[2 * j + 1]), h[2 * j + 1]);
         s.u[i][j][tid] = make_float4(u0.x, u0.y, u1.x, u1.y);
         h[2 * j] = fma2(w, low2(Bv), u0);
         h[2 * j + 1] = fma2(w, high2(Bv), u1);
@@ -498,8 +496,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) k_selective_scan_grad(const Se
           const float2 gu = mul2(g, lo ? low2(u) : high2(u));
           rr = fma2(A2[m], gu, rr);
           dA[m] = fma2(dd, gu, dA[m]);
-          const float2 t = mul2(dd, A2[m]);
-          q[m] = mul2(make_float2(ex2(t.x), ex2(t.y)), g);
+          q[m] = mul2(decay2(dd, A2[m]), g);
         }
       }
       Sum::run(v);
