@@ -377,35 +377,33 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
 
 // ----------------------------------------------------------------- decoding --
 
-// out[16 b + i] = E4M3(codes[16 b + i]) * 2^exps[b], rounded once to Ty.
-template <typename Ty>
-__global__ void __launch_bounds__(256) k_dequantize_fp8blk(const uint8_t* __restrict__ codes,
-                                                           const int8_t* __restrict__ exps, int64_t n_blocks,
-                                                           Ty* __restrict__ out) {
-  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < n_blocks;
-       b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float v[16];
-    fp8blk_unpack16(reinterpret_cast<const uint4*>(codes)[b], exps[b], v);
-    store8<Ty>(out + 16 * b, v);
-    store8<Ty>(out + 16 * b + 8, v + 8);
+// Eight codes (value i in byte i) times a scale.
+__device__ __forceinline__ void e4m3_values8(uint2 u, float scale, float* out) {
+  const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+    out[2 * i] = f.x * scale;
+    out[2 * i + 1] = f.y * scale;
   }
 }
 
-// out[r, c] = E4M3(codes[r, c]) * scales[r], rounded once to Ty; rows of whole
-// 16-value units.
-template <typename Ty>
-__global__ void __launch_bounds__(256) k_dequantize_fp8row(const uint8_t* __restrict__ codes,
-                                                           const float* __restrict__ scales, int64_t n_units,
-                                                           int units_per_row, Ty* __restrict__ out) {
-  for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < n_units;
-       b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float v[16];
-    fp8blk_unpack16(reinterpret_cast<const uint4*>(codes)[b], 0, v);
-    const float c = scales[b / units_per_row];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= c;
-    store8<Ty>(out + 16 * b, v);
-    store8<Ty>(out + 16 * b + 8, v + 8);
+// Values of E4M3 codes, rounded once to Ty: units of 8, so that neighbouring
+// threads' accesses touch on both sides. kBlocks: times 2^exps per 16 values,
+// else times a scale per row of units_per_row units.
+template <typename Ty, bool kBlocks>
+__global__ void __launch_bounds__(256) k_dequantize_fp8(const uint8_t* __restrict__ codes,
+                                                        const void* __restrict__ scales, int64_t n_units,
+                                                        int units_per_row, Ty* __restrict__ out) {
+  for (int64_t u = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; u < n_units;
+       u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const float scale = kBlocks ? pow2f(static_cast<const int8_t*>(scales)[u / 2])
+                                : static_cast<const float*>(scales)[u / units_per_row];
+    float v[8];
+    e4m3_values8(reinterpret_cast<const uint2*>(codes)[u], scale, v);
+    store8<Ty>(out + 8 * u, v);
   }
 }
 

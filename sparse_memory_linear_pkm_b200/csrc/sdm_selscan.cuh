@@ -346,19 +346,29 @@ static __global__ void __launch_bounds__(256) k_selective_scan_join(const float*
   if (i >= total) return;
   const int64_t b = i / per_b, r = i % per_b;
   float h = h0 == nullptr ? 0.f : h0[i];
-  constexpr int kAhead = 8;  // the loads of as many splits go out together
-  for (int s0 = 0; s0 < splits; s0 += kAhead) {
+  // The loads of kAhead splits go out together, before the states of the ones
+  // before them are chained and written.
+  constexpr int kAhead = 8;
+  float p[kAhead], q[kAhead];
+  auto fetch = [&](int s0) {
     const int64_t at = (b * splits + s0) * per_b + r;
-    float p[kAhead], q[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       p[j] = s0 + j < splits ? P[at + j * per_b] : 0.f;
       q[j] = s0 + j < splits ? H[at + j * per_b] : 0.f;
     }
+  };
+  fetch(0);
+  for (int s0 = 0; s0 < splits; s0 += kAhead) {
+    const int64_t at = (b * splits + s0) * per_b + r;
+    float p0[kAhead], q0[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) p0[j] = p[j], q0[j] = q[j];
+    fetch(s0 + kAhead);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (s0 + j < splits) H[at + j * per_b] = h;
-      h = fmaf(p[j], h, q[j]);
+      h = fmaf(p0[j], h, q0[j]);
     }
   }
 }

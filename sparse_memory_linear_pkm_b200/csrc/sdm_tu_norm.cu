@@ -99,6 +99,25 @@ void launch_norm_grad(const NormPlan& p, unsigned grid, const sdm::NormGradArgs&
   }
 }
 
+template <bool kBlocks>
+sdm_status_t dequantize(const uint8_t* codes, const void* scales, int64_t units, int units_per_row, void* out,
+                        int32_t out_dtype, void* stream) {
+  sdm_status_t r;
+  DeviceInfo* dev;
+  if ((r = device_info(&dev)) != SDM_OK) return r;
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>((units + 255) / 256, static_cast<int64_t>(dev->sms) * 64));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (out_dtype == SDM_BF16)
+    sdm::k_dequantize_fp8<bf16, kBlocks><<<grid, 256, 0, st>>>(codes, scales, units, units_per_row,
+                                                               static_cast<bf16*>(out));
+  else
+    sdm::k_dequantize_fp8<float, kBlocks><<<grid, 256, 0, st>>>(codes, scales, units, units_per_row,
+                                                                static_cast<float*>(out));
+  if ((r = launch_status("dequantize launch")) != SDM_OK) return r;
+  return ok();
+}
+
 }  // namespace
 
 }  // namespace sdm_host
@@ -154,16 +173,7 @@ sdm_status_t sdm_dequantize_fp8blk(const uint8_t* codes, const int8_t* exps, int
   if ((r = need_ptr(codes, "codes", any)) || (r = need_ptr(out, "out", any))) return r;
   if (any && exps == nullptr) return fail(SDM_ERR_INVALID_ARGUMENT, "exps is NULL");
   if (!any) return ok();
-  DeviceInfo* dev;
-  if ((r = device_info(&dev)) != SDM_OK) return r;
-  const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>((n_blocks + 255) / 256, static_cast<int64_t>(dev->sms) * 32));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (out_dtype == SDM_BF16)
-    sdm::k_dequantize_fp8blk<bf16><<<grid, 256, 0, st>>>(codes, exps, n_blocks, static_cast<bf16*>(out));
-  else sdm::k_dequantize_fp8blk<float><<<grid, 256, 0, st>>>(codes, exps, n_blocks, static_cast<float*>(out));
-  if ((r = launch_status("dequantize_fp8blk launch")) != SDM_OK) return r;
-  return ok();
+  return dequantize<true>(codes, exps, 2 * n_blocks, 2, out, out_dtype, stream);
 }
 
 sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, int64_t n_rows, int32_t d, void* out,
@@ -177,17 +187,7 @@ sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, in
       (r = need_ptr(out, "out", any)))
     return r;
   if (!any) return ok();
-  DeviceInfo* dev;
-  if ((r = device_info(&dev)) != SDM_OK) return r;
-  const int64_t units = n_rows * (d / 16);
-  const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>((units + 255) / 256, static_cast<int64_t>(dev->sms) * 32));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (out_dtype == SDM_BF16)
-    sdm::k_dequantize_fp8row<bf16><<<grid, 256, 0, st>>>(codes, scales, units, d / 16, static_cast<bf16*>(out));
-  else sdm::k_dequantize_fp8row<float><<<grid, 256, 0, st>>>(codes, scales, units, d / 16, static_cast<float*>(out));
-  if ((r = launch_status("dequantize_fp8row launch")) != SDM_OK) return r;
-  return ok();
+  return dequantize<false>(codes, scales, n_rows * (d / 8), d / 8, out, out_dtype, stream);
 }
 
 size_t sdm_rmsnorm_residual_backward_workspace_bytes(int64_t n_rows, int32_t d) {
