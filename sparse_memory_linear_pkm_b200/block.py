@@ -79,7 +79,7 @@ def _needed(lib, nbytes: int, nonempty: bool) -> int:
 
 
 def _token_stride(t: torch.Tensor, inner: int, what: str) -> int:
-    """Elements from token to token of a [B, T, ...] tensor whose axes behind the second hold `inner` elements in order."""
+    """Elements from token to token of a [B, T, ...] tensor whose later axes hold `inner` elements in order."""
     if t.is_contiguous():
         return inner
     shape, stride = t.shape, t.stride()

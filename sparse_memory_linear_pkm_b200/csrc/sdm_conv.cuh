@@ -82,7 +82,8 @@ __device__ __forceinline__ void conv_bias(const void* p, int bf, int c0, int n, 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     v[i] = 0.f;
-    if (p != nullptr && i < n) v[i] = bf ? to_f32<bf16>(static_cast<const bf16*>(p)[c0 + i]) : static_cast<const float*>(p)[c0 + i];
+    if (p != nullptr && i < n)
+      v[i] = bf ? to_f32<bf16>(static_cast<const bf16*>(p)[c0 + i]) : static_cast<const float*>(p)[c0 + i];
   }
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) out[i] = make_float2(v[2 * i], v[2 * i + 1]);
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
     const int t = t0 - (KT - 1) + i;
     old[i].zero();
     if (t >= 0) conv_load<T, V, kVec>(old[i], x + t * a.x_stride, n);
-    else if (t >= -hist && state != nullptr) conv_load<T, V, kVec>(old[i], state + static_cast<int64_t>(hist + t) * a.D, n);
+    else if (t >= -hist && state != nullptr)
+      conv_load<T, V, kVec>(old[i], state + static_cast<int64_t>(hist + t) * a.D, n);
   }
   const T* ahead = x + t0 * a.x_stride;  // of the tokens to be loaded next, from `left` before the run's end
   int left = t1 - t0;
@@ -172,7 +174,8 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) {
       const int t = len - hist + j;
-      if (j < hist) conv_load<T, V, kVec>(row[j], t >= 0 ? x + t * a.x_stride : state + static_cast<int64_t>(hist + t) * a.D, n);
+      if (j < hist)
+        conv_load<T, V, kVec>(row[j], t >= 0 ? x + t * a.x_stride : state + static_cast<int64_t>(hist + t) * a.D, n);
     }
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j)

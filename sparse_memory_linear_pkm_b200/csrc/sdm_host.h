@@ -1,7 +1,9 @@
 // Host-side declarations shared by the translation units of libsdm_b200.so
-// (internal: none of this is part of the C ABI in sdm.h). The entry points
-// live in sdm_api.cu; the launches of kernels with many template instances
-// live in sdm_tu_*.cu so that the library compiles in parallel.
+// (internal: none of this is part of the C ABI in sdm.h). The core's entry
+// points live in sdm_api.cu, those of the operators around it (norm, short
+// convolution, selective scan, clipping) in their own sdm_tu_*.cu; the launches
+// of kernels with many template instances live in sdm_tu_*.cu too, so that the
+// library compiles in parallel.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -116,7 +116,8 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
   const bool vec = whole_units(x, stride, D, in_dtype);
   const int units = static_cast<int>(ceil_div(D, sdm::kConvV)), run = conv_run(B, T, units);
   const sdm::ConvArgs a{x, w, bias, state, lengths, y, stride, T, D, K, units, run,
-                        static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
+                        static_cast<unsigned>(units * ceil_div(T, run)), w_dtype == SDM_BF16,
+                        whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (in_dtype == SDM_BF16) launch_conv<bf16>(vec, a, B, st);
   else launch_conv<float>(vec, a, B, st);
@@ -179,7 +180,8 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   const bool vec = whole_units(x, stride, D, in_dtype);
   float* part = static_cast<float*>(workspace);
   const sdm::ConvGradArgs a{x, w, bias, state0, dy, dstate, lengths, dx, dstate0, part, stride, B, T, D, K,
-                            static_cast<int>(ceil_div(D, sdm::kConvV)), p.segs, kGradSeg, w_dtype == SDM_BF16, whole_taps(w, w_dtype, K), silu != 0, dev->err};
+                            static_cast<int>(ceil_div(D, sdm::kConvV)), p.segs, kGradSeg, w_dtype == SDM_BF16,
+                            whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const dim3 grid(static_cast<unsigned>(ceil_div(a.units, sdm::kConvGradLanes)), static_cast<unsigned>(p.slots));
   if (in_dtype == SDM_BF16) {
     if (K <= 4) launch_conv_grad_taps<bf16, 4>(vec, a, grid, st);

@@ -20,10 +20,10 @@ struct SelPlan {
 };
 
 // Splitting makes every exponential twice, so it pays where the channels leave
-// most of the device idle: with w warps an SM one pass takes about 1.14 / w
-// clocks per exponential (0.41 at 2.6, 0.165 at 6.9), two take 0.19 once some
-// 30 warps an SM are there (0.178 at B = 8, T = 4096, D = 4096; 0.198 at B = 1,
-// T = 16384, D = 2048).
+// most of the device idle: with w warps an SM one pass takes about 0.95 / w
+// clocks per exponential (0.35 at 2.6, 0.143 at 6.9), two take 0.17 to 0.19 once
+// some 30 warps an SM are there (0.171 at B = 8, T = 4096, D = 4096; 0.188 at B =
+// 6, T = 2047, D = 2048).
 SelPlan sel_plan(const sdm_selscan_shape_t& s) {
   SelPlan p;
   p.step = s.T <= kStepTokens;

@@ -159,7 +159,8 @@ struct RawUnit {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       v[i] = 0u;
-      if (i < n) v[i] = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(p)[i] : reinterpret_cast<const uint16_t*>(p)[i];
+      if (i < n)
+        v[i] = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(p)[i] : reinterpret_cast<const uint16_t*>(p)[i];
     }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? v[i % V] : v[2 * i % V] | v[(2 * i + 1) % V] << 16;
