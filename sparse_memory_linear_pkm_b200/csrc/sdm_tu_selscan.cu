@@ -9,9 +9,15 @@ namespace {
 // Tokens a sequence may have for the kernel without shared memory: there each
 // token waits for its own loads.
 constexpr int kStepTokens = 4;
-// A split of the token axis has at least this many tokens: its map costs the
-// bandwidth of about 30.
-constexpr int kSplitTokens = 128;
+// The token axis is split until there are so many warps an SM, while a split
+// keeps so many tokens. A split costs the time of some ten tokens for its map and
+// an unhidden start of its loads, so that short ones pay only where there are few
+// warps. Measured in bf16 with N = 16: 64 warps instead of 32, 65,536 x 2048 1385
+// -> 1341 us; 64 tokens instead of 128, 1000 x 4096 73 -> 60; 32 tokens instead of
+// 64, 384 x 1024 29 -> 20. 64 tokens up to 48 warps: 8192 x 1536 147 -> 155; 32
+// tokens up to 48 warps: 4096 x 2048 103 -> 110.
+struct SelSplit { int warps, tokens; };
+constexpr SelSplit kSelSplits[] = {{64, 128}, {32, 64}, {16, 32}};
 
 struct SelPlan {
   bool step = false;
@@ -22,8 +28,8 @@ struct SelPlan {
 // Splitting makes every exponential twice, so it pays where the channels leave
 // most of the device idle: with w warps an SM one pass takes about 0.95 / w
 // clocks per exponential (0.35 at 2.6, 0.143 at 6.9), two take 0.17 to 0.19 once
-// some 30 warps an SM are there (0.171 at B = 8, T = 4096, D = 4096; 0.188 at B =
-// 6, T = 2047, D = 2048).
+// some 30 warps an SM are there. At 4.3 warps (B = 5, T = 4096, D = 4096): one
+// pass 1068 us, two 871; at 5.2 (B = 6) 1078 and 1028; at 6 and above one pass.
 SelPlan sel_plan(const sdm_selscan_shape_t& s) {
   SelPlan p;
   p.step = s.T <= kStepTokens;
@@ -32,8 +38,10 @@ SelPlan sel_plan(const sdm_selscan_shape_t& s) {
   const int64_t warps =
       static_cast<int64_t>(s.B) * s.G * ceil_div(s.D / s.G, sel_channels(s.N)) * (sdm::kSelThreads / 32);
   if (warps >= 6 * kSms) return p;
-  const int64_t splits = std::min<int64_t>(32 * kSms / warps, s.T / kSplitTokens);
-  if (splits < 3) return p;
+  int64_t splits = 0;
+  for (const SelSplit& l : kSelSplits)
+    splits = std::max(splits, std::min<int64_t>(l.warps * kSms / warps, s.T / l.tokens));
+  if (splits < 4) return p;
   const int tile = sdm::kSelTile;
   p.tokens_per_split = static_cast<int>(ceil_div(ceil_div(s.T, splits), tile) * tile);
   p.splits = static_cast<int>(ceil_div(s.T, p.tokens_per_split));
