@@ -567,7 +567,9 @@ SDM_API size_t sdm_selective_scan_workspace_bytes(const sdm_selscan_shape_t* sha
  *   x, dt, z [B,T,D], Bm, Cm [B,T,G,N] in_dtype, aligned to their element; z
  *     may be NULL (no gate)
  *   A [D,N], Dskip [D] or NULL, dt_bias [D] or NULL: fp32. A is finite and, for
- *     a state that decays, negative.
+ *     a state that decays, negative. Long sequences are computed in parts, each
+ *     part's decays as one factor: where delta A sums to more than 88 in a part
+ *     (growing states), that factor, and what it multiplies, is not finite.
  *   lengths [B] int32 or NULL, as in sdm_short_conv
  *   h0 [B,D,N] fp32 or NULL (zeros): the state before the first token;
  *   hT [B,D,N] fp32 or NULL: the state after each row's last token; may be h0,

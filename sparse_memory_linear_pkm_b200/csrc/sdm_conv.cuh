@@ -48,31 +48,31 @@ __device__ __forceinline__ int clamp_length(const int32_t* lengths, int b, int T
   return n;
 }
 
-// The KT-tap window of V channels from c0, as channel pairs, of which n exist:
-// the K given taps are the last K of KT, the ones before them are 0. `whole`:
-// K = KT = 4 and a channel's taps are one aligned unit.
-template <int KT, int V>
-__device__ __forceinline__ void conv_weights(const void* w, int bf, bool whole, int c0, int n, int K,
+// The K taps of V channels from c0, as channel pairs, of which n exist. `whole`:
+// K = 4 and a channel's taps are one aligned unit. (K is the number of taps
+// itself, for each of its values: taps of 0 before them would bring an infinite
+// input into outputs that do not depend on it.)
+template <int K, int V>
+__device__ __forceinline__ void conv_weights(const void* w, int bf, bool whole, int c0, int n,
                                              float2 (*out)[V / 2]) {
-  float v[V][KT];
+  float v[V][K];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int64_t at = static_cast<int64_t>(c0 + i) * K;
-    if (KT == 4 && whole && i < n) {
+    if (K == 4 && whole && i < n) {
       if (bf) load_unit<bf16, 4>(static_cast<const bf16*>(w) + at, v[i]);
       else load_unit<float, 4>(static_cast<const float*>(w) + at, v[i]);
     } else {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const int tap = k - (KT - K);
+      for (int k = 0; k < K; ++k) {
         v[i][k] = 0.f;
-        if (tap >= 0 && i < n)
-          v[i][k] = bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at + tap]) : static_cast<const float*>(w)[at + tap];
+        if (i < n)
+          v[i][k] = bf ? to_f32<bf16>(static_cast<const bf16*>(w)[at + k]) : static_cast<const float*>(w)[at + k];
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < KT; ++k)
+  for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) out[k][i] = make_float2(v[2 * i][k], v[2 * i + 1][k]);
 }
@@ -119,11 +119,11 @@ constexpr int kConvV = 2;
 constexpr int kConvAhead = 4;  // tokens loaded together, one such run before they are used
 static_assert(kConvMaxK - 1 <= 2 * kConvAhead, "runs are at least two of these, so only the first reaches the state");
 
-// A thread walks one run of tokens of kConvV channels with the last KT - 1
+// A thread walks one run of tokens of kConvV channels with the last K - 1
 // inputs in registers. The thread of a sequence's first run also moves the
 // state: it alone reads the old one, and the new one comes from x and the old
 // one, so both may be one buffer.
-template <typename T, int KT, bool kVec>
+template <typename T, int K, bool kVec>
 __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
   constexpr int V = kConvV, P = V / 2;
   const unsigned id = blockIdx.x * blockDim.x + threadIdx.x;
@@ -132,23 +132,23 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
   const int unit = static_cast<int>(id) - run * a.units, b = blockIdx.y;
   const int c0 = unit * V, n = a.D - c0, t0 = run * a.run;
   const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride + c0;
-  const int hist = a.K - 1;
+  constexpr int hist = K - 1;
   T* state = a.state == nullptr ? nullptr : static_cast<T*>(a.state) + static_cast<int64_t>(b) * hist * a.D + c0;
 
-  float2 w[KT][P], bias[P];
-  conv_weights<KT, V>(a.w, a.w_bf16, a.w_whole, c0, n, a.K, w);
+  float2 w[K][P], bias[P];
+  conv_weights<K, V>(a.w, a.w_bf16, a.w_whole, c0, n, w);
   conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
   const int len = clamp_length(a.lengths, b, a.T, a.err);
   const int t1 = min(len, t0 + a.run);
   if (t0 >= len && run != 0) return;
 
-  RawUnit<T, V> old[KT - 1], next[kConvAhead];
+  RawUnit<T, V> old[K - 1], next[kConvAhead];
 #pragma unroll
-  for (int i = 0; i < KT - 1; ++i) {
-    const int t = t0 - (KT - 1) + i;
+  for (int i = 0; i < K - 1; ++i) {
+    const int t = t0 - hist + i;
     old[i].zero();
     if (t >= 0) conv_load<T, V, kVec>(old[i], x + t * a.x_stride, n);
-    else if (t >= -hist && state != nullptr)
+    else if (state != nullptr)
       conv_load<T, V, kVec>(old[i], state + static_cast<int64_t>(hist + t) * a.D, n);
   }
   const T* ahead = x + t0 * a.x_stride;  // of the tokens to be loaded next, from `left` before the run's end
@@ -170,25 +170,23 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
   if (run == 0 && state != nullptr) {
     // Row j of the new state is input len - hist + j, of the old state where
     // that is negative: row len + j of it. All are read before any is written.
-    RawUnit<T, V> row[KT - 1];
+    RawUnit<T, V> row[K - 1];
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j) {
+    for (int j = 0; j < K - 1; ++j) {
       const int t = len - hist + j;
-      if (j < hist)
-        conv_load<T, V, kVec>(row[j], t >= 0 ? x + t * a.x_stride : state + static_cast<int64_t>(hist + t) * a.D, n);
+      conv_load<T, V, kVec>(row[j], t >= 0 ? x + t * a.x_stride : state + static_cast<int64_t>(hist + t) * a.D, n);
     }
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j)
-      if (j < hist) {
-        float2 v[P];
+    for (int j = 0; j < K - 1; ++j) {
+      float2 v[P];
 #pragma unroll
-        for (int p = 0; p < P; ++p) v[p] = row[j].pair(p);
-        conv_store<T, V, kVec>(state + static_cast<int64_t>(j) * a.D, n, v);
-      }
+      for (int p = 0; p < P; ++p) v[p] = row[j].pair(p);
+      conv_store<T, V, kVec>(state + static_cast<int64_t>(j) * a.D, n, v);
+    }
   }
-  float2 win[KT - 1 + kConvAhead][P];
+  float2 win[K - 1 + kConvAhead][P];
 #pragma unroll
-  for (int i = 0; i < KT - 1; ++i)
+  for (int i = 0; i < K - 1; ++i)
 #pragma unroll
     for (int p = 0; p < P; ++p) win[i][p] = old[i].pair(p);
   T* y = static_cast<T*>(a.y) + (static_cast<int64_t>(b) * a.T + t0) * a.D + c0;
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
 #pragma unroll
     for (int i = 0; i < kConvAhead; ++i)
 #pragma unroll
-      for (int p = 0; p < P; ++p) win[KT - 1 + i][p] = next[i].pair(p);
+      for (int p = 0; p < P; ++p) win[K - 1 + i][p] = next[i].pair(p);
     fetch();
 #pragma unroll
     for (int i = 0; i < kConvAhead; ++i) {
@@ -205,14 +203,14 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
       for (int p = 0; p < P; ++p) {
         o[p] = bias[p];
 #pragma unroll
-        for (int k = 0; k < KT; ++k) o[p] = fma2(w[k][p], win[i + k][p], o[p]);
+        for (int k = 0; k < K; ++k) o[p] = fma2(w[k][p], win[i + k][p], o[p]);
         if (a.silu) o[p] = silu2(o[p]);
       }
       if (t + i < t1) conv_store<T, V, kVec>(y, n, o);
       y += a.D;
     }
 #pragma unroll
-    for (int i = 0; i < KT - 1; ++i)
+    for (int i = 0; i < K - 1; ++i)
 #pragma unroll
       for (int p = 0; p < P; ++p) win[i][p] = win[kConvAhead + i][p];
   }
@@ -249,36 +247,36 @@ constexpr int kConvGradLanes = 32, kConvGradRows = 8;   // units x segments of a
 // 0.40 GB of B = 8, T = 4096, D = 2048 in bf16 (3.6 TB/s): 33 instructions a
 // value keep the issue slots 58 % busy at 24 warps an SM. (128 registers and 16
 // warps: 132 us.)
-template <typename T, int KT, bool kVec>
-__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, KT == 4 ? 3 : 1)
+template <typename T, int K, bool kVec>
+__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, K <= 4 ? 3 : 1)
     k_short_conv_backward(const ConvGradArgs a) {
   constexpr int V = kConvV, kAhead = kConvAhead;
-  __shared__ float2 sums[kConvGradRows][KT + 1][kConvGradLanes];
+  __shared__ float2 sums[kConvGradRows][K + 1][kConvGradLanes];
   const int lane = threadIdx.x, row = threadIdx.y;
   const int unit = blockIdx.x * kConvGradLanes + lane, c0 = unit * V, n = a.D - c0;
   const int64_t s = static_cast<int64_t>(blockIdx.y) * kConvGradRows + row;
-  float2 dw[KT], db = both(0.f);
+  float2 dw[K], db = both(0.f);
 #pragma unroll
-  for (int k = 0; k < KT; ++k) dw[k] = both(0.f);
+  for (int k = 0; k < K; ++k) dw[k] = both(0.f);
   if (unit < a.units && s < static_cast<int64_t>(a.B) * a.segs) {
     const int b = static_cast<int>(s / a.segs), t0 = static_cast<int>(s % a.segs) * a.seg;
     const int t1 = min(a.T, t0 + a.seg);
-    const int hist = a.K - 1;
-    float2 w[KT][1], bias[1];
-    conv_weights<KT, V>(a.w, a.w_bf16, a.w_whole, c0, n, a.K, w);
+    constexpr int hist = K - 1;
+    float2 w[K][1], bias[1];
+    conv_weights<K, V>(a.w, a.w_bf16, a.w_whole, c0, n, w);
     conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
     const int len = clamp_length(a.lengths, b, a.T, a.err);
     const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.T * a.x_stride + c0;
     const T* dy = static_cast<const T*>(a.dy) + static_cast<int64_t>(b) * a.T * a.D + c0;
     T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(b) * a.T * a.D + c0;
     const int64_t sb = static_cast<int64_t>(b) * hist * a.D + c0;
-    // Slot j of xw and du is token t - (KT - 1) + j, t the first of a run of
+    // Slot j of xw and du is token t - (K - 1) + j, t the first of a run of
     // kAhead; du before the segment is not needed (another segment's outputs).
-    float2 xw[KT - 1 + kAhead], du[KT - 1 + kAhead];
+    float2 xw[K - 1 + kAhead], du[K - 1 + kAhead];
     RawUnit<T, V> rx[kAhead], rd[kAhead], r;
     const T* x_next = x + t0 * a.x_stride;  // of the tokens to be loaded next, from `left` before the last one needed
     const T* dy_next = dy + static_cast<int64_t>(t0) * a.D;
-    int left = min(len, t1 + KT - 1) - t0;
+    int left = min(len, t1 + K - 1) - t0;
     auto fetch = [&]() {
       if (left >= kAhead) {
 #pragma unroll
@@ -301,26 +299,27 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, KT == 4 ? 3 : 
     };
     fetch();
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j) {
-      const int t = t0 - (KT - 1) + j;
+    for (int j = 0; j < K - 1; ++j) {
+      const int t = t0 - (K - 1) + j;
       du[j] = both(0.f);
       r.zero();
       if (t >= 0 && t < len) conv_load<T, V, kVec>(r, x + t * a.x_stride, n);
-      else if (t < 0 && t >= -hist && a.state0 != nullptr)
+      else if (t < 0 && a.state0 != nullptr)
         conv_load<T, V, kVec>(r, static_cast<const T*>(a.state0) + sb + static_cast<int64_t>(hist + t) * a.D, n);
       xw[j] = r.pair(0);
     }
-    // Token t's du completes dx of token t - (KT - 1). The first segment also
+    // Token t's du completes dx of token t - (K - 1). The first segment also
     // finishes the K - 1 rows before token 0. Inside the segment (kIn) every
     // token of a step counts and every output is an ordinary row.
+    const int stop = min(t1, len);  // tokens that count in the sums
     const int last = a.dstate == nullptr ? t1 : min(t1, len - hist);  // dx rows that the final state does not reach
-    T* out = dx + static_cast<int64_t>(t0 - (KT - 1)) * a.D;          // row `to` of the next output
+    T* out = dx + static_cast<int64_t>(t0 - (K - 1)) * a.D;          // row `to` of the next output
     auto step = [&](int t, auto in) {
       constexpr bool kIn = decltype(in)::value;
       float2 dn[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        xw[KT - 1 + i] = rx[i].pair(0);
+        xw[K - 1 + i] = rx[i].pair(0);
         dn[i] = rd[i].pair(0);
       }
       fetch();
@@ -330,20 +329,20 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, KT == 4 ? 3 : 
         if (a.silu && (kIn || t + i < len)) {
           float2 u = bias[0];
 #pragma unroll
-          for (int k = 0; k < KT; ++k) u = fma2(w[k][0], xw[i + k], u);
+          for (int k = 0; k < K; ++k) u = fma2(w[k][0], xw[i + k], u);
           g = mul2(g, silu_grad2(u));
         }
-        du[KT - 1 + i] = g;
-        if (kIn || t + i < t1) {
+        du[K - 1 + i] = g;
+        if (kIn || t + i < stop) {
           db = add2(db, g);
 #pragma unroll
-          for (int k = 0; k < KT; ++k) dw[k] = fma2(g, xw[i + k], dw[k]);
+          for (int k = 0; k < K; ++k) dw[k] = fma2(g, xw[i + k], dw[k]);
         }
-        const int to = t + i - (KT - 1);  // its window of du is complete now
+        const int to = t + i - (K - 1);  // its window of du is complete now
         if (kIn || (to < t1 && (to >= t0 || (t0 == 0 && to >= -hist)))) {
           float2 o = both(0.f);
 #pragma unroll
-          for (int k = 0; k < KT; ++k) o = fma2(w[k][0], du[i + KT - 1 - k], o);
+          for (int k = 0; k < K; ++k) o = fma2(w[k][0], du[i + K - 1 - k], o);
           if (!kIn && a.dstate != nullptr) {
             // Input `to` is row to - (len - hist) of the final state.
             const int j = to - (len - hist);
@@ -359,29 +358,29 @@ __global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, KT == 4 ? 3 : 
         out += a.D;
       }
 #pragma unroll
-      for (int j = 0; j < KT - 1; ++j) xw[j] = xw[kAhead + j], du[j] = du[kAhead + j];
+      for (int j = 0; j < K - 1; ++j) xw[j] = xw[kAhead + j], du[j] = du[kAhead + j];
     };
-    for (int t = t0; t < t1 + KT - 1; t += kAhead) {
-      if (t - (KT - 1) >= t0 && t + kAhead <= min(t1, len) && t + kAhead - (KT - 1) <= last) step(t, std::true_type());
+    for (int t = t0; t < t1 + K - 1; t += kAhead) {
+      if (t - (K - 1) >= t0 && t + kAhead <= stop && t + kAhead - (K - 1) <= last) step(t, std::true_type());
       else step(t, std::false_type());
     }
   }
 #pragma unroll
-  for (int k = 0; k < KT; ++k) sums[row][k][lane] = dw[k];
-  sums[row][KT][lane] = db;
+  for (int k = 0; k < K; ++k) sums[row][k][lane] = dw[k];
+  sums[row][K][lane] = db;
   __syncthreads();
   const int tid = row * kConvGradLanes + lane;
-  for (int i = tid; i < (a.K + 1) * kConvGradLanes * V; i += kConvGradLanes * kConvGradRows) {
-    const int cc = i / (a.K + 1), k = i % (a.K + 1);
+  for (int i = tid; i < (K + 1) * kConvGradLanes * V; i += kConvGradLanes * kConvGradRows) {
+    const int cc = i / (K + 1), k = i % (K + 1);
     const int c = blockIdx.x * kConvGradLanes * V + cc;
     if (c < a.D) {
       float v = 0.f;
 #pragma unroll
       for (int q = 0; q < kConvGradRows; ++q) {
-        const float2 f = sums[q][k < a.K ? k + KT - a.K : KT][cc / 2];
+        const float2 f = sums[q][k][cc / 2];
         v += cc % 2 == 0 ? f.x : f.y;
       }
-      a.part[(static_cast<int64_t>(blockIdx.y) * a.D + c) * (a.K + 1) + k] = v;
+      a.part[(static_cast<int64_t>(blockIdx.y) * a.D + c) * (K + 1) + k] = v;
     }
   }
 }

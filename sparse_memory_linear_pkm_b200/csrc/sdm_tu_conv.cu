@@ -2,6 +2,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "sdm_check.h"
 #include "sdm_conv.cuh"
@@ -42,11 +43,13 @@ bool whole_taps(const void* w, int32_t dtype, int32_t K) {
   return K == 4 && reinterpret_cast<uintptr_t>(w) % (4 * in_size(dtype)) == 0;
 }
 
-template <typename T, int KT>
-void launch_conv_taps(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.per_seq, 256)), B);
-  if (vec) sdm::k_short_conv<T, KT, true><<<grid, 256, 0, st>>>(a);
-  else sdm::k_short_conv<T, KT, false><<<grid, 256, 0, st>>>(a);
+// f(std::integral_constant<int, K>()) for the K in [2, kConvMaxK] of a call.
+template <int kTaps = 2, typename F>
+void with_taps(int K, const F& f) {
+  if constexpr (kTaps < sdm::kConvMaxK) {
+    if (K != kTaps) return with_taps<kTaps + 1>(K, f);
+  }
+  f(std::integral_constant<int, kTaps>());
 }
 
 // Tokens of a thread: up to 64 (the K - 1 inputs before a run are read twice),
@@ -59,15 +62,20 @@ int conv_run(int B, int T, int units) {
 
 template <typename T>
 void launch_conv(bool vec, const sdm::ConvArgs& a, int B, cudaStream_t st) {
-  if (a.K <= 4) launch_conv_taps<T, 4>(vec, a, B, st);
-  else launch_conv_taps<T, 8>(vec, a, B, st);
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.per_seq, 256)), B);
+  with_taps(a.K, [&](auto K) {
+    if (vec) sdm::k_short_conv<T, K.value, true><<<grid, 256, 0, st>>>(a);
+    else sdm::k_short_conv<T, K.value, false><<<grid, 256, 0, st>>>(a);
+  });
 }
 
-template <typename T, int KT>
-void launch_conv_grad_taps(bool vec, const sdm::ConvGradArgs& a, dim3 grid, cudaStream_t st) {
+template <typename T>
+void launch_conv_grad(bool vec, const sdm::ConvGradArgs& a, dim3 grid, cudaStream_t st) {
   const dim3 block(sdm::kConvGradLanes, sdm::kConvGradRows);
-  if (vec) sdm::k_short_conv_backward<T, KT, true><<<grid, block, 0, st>>>(a);
-  else sdm::k_short_conv_backward<T, KT, false><<<grid, block, 0, st>>>(a);
+  with_taps(a.K, [&](auto K) {
+    if (vec) sdm::k_short_conv_backward<T, K.value, true><<<grid, block, 0, st>>>(a);
+    else sdm::k_short_conv_backward<T, K.value, false><<<grid, block, 0, st>>>(a);
+  });
 }
 
 struct ConvGradPlan {
@@ -183,13 +191,8 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
                             static_cast<int>(ceil_div(D, sdm::kConvV)), p.segs, kGradSeg, w_dtype == SDM_BF16,
                             whole_taps(w, w_dtype, K), silu != 0, dev->err};
   const dim3 grid(static_cast<unsigned>(ceil_div(a.units, sdm::kConvGradLanes)), static_cast<unsigned>(p.slots));
-  if (in_dtype == SDM_BF16) {
-    if (K <= 4) launch_conv_grad_taps<bf16, 4>(vec, a, grid, st);
-    else launch_conv_grad_taps<bf16, 8>(vec, a, grid, st);
-  } else {
-    if (K <= 4) launch_conv_grad_taps<float, 4>(vec, a, grid, st);
-    else launch_conv_grad_taps<float, 8>(vec, a, grid, st);
-  }
+  if (in_dtype == SDM_BF16) launch_conv_grad<bf16>(vec, a, grid, st);
+  else launch_conv_grad<float>(vec, a, grid, st);
   if ((r = launch_status("short_conv_backward launch")) != SDM_OK) return r;
   const int64_t n = static_cast<int64_t>(D) * (K + 1);
   sdm::k_short_conv_sums<<<static_cast<unsigned>(ceil_div(n, 32)), dim3(32, 8), 0, st>>>(part, p.slots, D, K, dw,

@@ -152,3 +152,33 @@ def test_empty(sdm):
     assert sdm.short_conv(x, w, b, state=s).shape == (2, 0, 8) and torch.equal(s, before)
     got = sdm.short_conv_backward(x, w, x, b, state0=s, dstate=s)
     assert not got["dw"].any() and not got["dbias"].any() and torch.equal(got["dstate0"], s)
+
+
+@pytest.mark.parametrize("K", [2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("dtype,D", [(BF16, 6), (F32, 5)])
+def test_infinite_values_stay_in_their_window(sdm, K, dtype, D):
+    """An infinite input reaches the K outputs that depend on it, an infinite dy the K inputs it depends on, and an
+    infinite last input of a row no tap's gradient but the last one's: all others keep their bits."""
+    x, w, b, _, n = make(2, 90, D, K, dtype, state=False, lengths=[90, 70], seed=K)
+    dy = torch.randn(2, 90, D, generator=torch.Generator().manual_seed(K + 50)).to(dtype).cuda()
+    at = 63  # its window crosses the runs of tokens
+    bad = x.clone()
+    bad[0, at] = float("inf")
+    bad[1, 69] = float("inf")
+    clean_y, y = sdm.short_conv(x, w, b, lengths=n), sdm.short_conv(bad, w, b, lengths=n)
+    assert torch.equal(y[0, :at], clean_y[0, :at]) and torch.equal(y[0, at + K:], clean_y[0, at + K:])
+    assert torch.equal(y[1, :69], clean_y[1, :69]) and torch.equal(y[1, 70:], clean_y[1, 70:])
+
+    bad_dy = dy.clone()
+    bad_dy[0, at] = float("inf")
+    clean = sdm.short_conv_backward(x, w, dy, b, silu=False, lengths=n)
+    dx = sdm.short_conv_backward(x, w, bad_dy, b, silu=False, lengths=n)["dx"]
+    assert torch.equal(dx[0, :at - K + 1], clean["dx"][0, :at - K + 1])
+    assert torch.equal(dx[0, at + 1:], clean["dx"][0, at + 1:]) and torch.equal(dx[1], clean["dx"][1])
+
+    bad = x.clone()
+    bad[1, 69] = float("inf")
+    got = sdm.short_conv_backward(bad, w, dy, b, silu=False, lengths=n)
+    assert torch.equal(got["dw"][:, :K - 1], clean["dw"][:, :K - 1]) and not got["dw"][:, K - 1].isfinite().any()
+    assert torch.equal(got["dx"], clean["dx"]) and torch.equal(got["dbias"], clean["dbias"])
+    sdm.stream_check()
