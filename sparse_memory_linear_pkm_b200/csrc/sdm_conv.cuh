@@ -248,7 +248,7 @@ constexpr int kConvGradLanes = 32, kConvGradRows = 8;   // units x segments of a
 // value keep the issue slots 58 % busy at 24 warps an SM. (128 registers and 16
 // warps: 132 us.)
 template <typename T, int K, bool kVec>
-__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, K <= 4 ? 3 : 1)
+__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, K <= 4 ? 3 : 2)
     k_short_conv_backward(const ConvGradArgs a) {
   constexpr int V = kConvV, kAhead = kConvAhead;
   __shared__ float2 sums[kConvGradRows][K + 1][kConvGradLanes];
