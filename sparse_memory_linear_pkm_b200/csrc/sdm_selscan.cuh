@@ -387,11 +387,12 @@ static __global__ void __launch_bounds__(256) k_selective_scan_join(const float*
 }
 
 // A few tokens per sequence (decoding): the state's way through memory is the
-// whole cost, so a thread takes a channel's states straight from it, walks the
-// tokens and writes them back; no shared memory. All of a thread's loads go out
-// before the first is used. (Four states a lane, as neighbouring lanes would
-// read them, make the step size and the gate four times: 24.5 us, bound by
-// issue, instead of 20.1 for B = 128, D = 4096, N = 16.)
+// whole cost, so a thread takes eight of a channel's states, a 32-byte sector,
+// straight from it, walks the tokens and writes them back; no shared memory. All
+// of a thread's loads go out before the first is used. 18.4 us for the 71 MB of B
+// = 128, D = 4096, N = 16, 3.9 TB/s. (Sixteen states a lane: 20.6 us, a sector's
+// halves and too few warps; four: 25.3, the step size and the gate are made four
+// times. N = 32: 27 us instead of 35 with sixteen; N = 12: 14.8 instead of 12.9.)
 constexpr int kStepThreads = 128;
 
 template <typename T, int KS, int L>

@@ -65,9 +65,9 @@ void launch_step(const sdm::SelScanArgs& a, int B, cudaStream_t st) {
     return dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.D) * lanes, threads)), B);
   };
   if (a.N <= 8) sdm::k_selective_scan_step<T, 8, 1><<<grid(1), threads, 0, st>>>(a);
-  else if (a.N <= 16) sdm::k_selective_scan_step<T, 16, 1><<<grid(1), threads, 0, st>>>(a);
-  else if (a.N <= 32) sdm::k_selective_scan_step<T, 16, 2><<<grid(2), threads, 0, st>>>(a);
-  else sdm::k_selective_scan_step<T, 16, 4><<<grid(4), threads, 0, st>>>(a);
+  else if (a.N <= 16) sdm::k_selective_scan_step<T, 8, 2><<<grid(2), threads, 0, st>>>(a);
+  else if (a.N <= 32) sdm::k_selective_scan_step<T, 8, 4><<<grid(4), threads, 0, st>>>(a);
+  else sdm::k_selective_scan_step<T, 8, 8><<<grid(8), threads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -108,7 +108,7 @@ sdm_status_t check_selscan(const sdm_selscan_shape_t* s) {
     return fail(SDM_ERR_INVALID_ARGUMENT, "b_stride and c_stride must be 0 or at least G * N");
   if (s->B > 65535) return fail(SDM_ERR_UNSUPPORTED, "B above 65535");
   if (s->T > INT32_MAX - 4096) return fail(SDM_ERR_UNSUPPORTED, "T above 2^31 - 4096");
-  // Thread numbers along the channels are 32-bit (4 lanes a channel at most).
+  // Thread numbers along the channels are 32-bit (8 lanes a channel at most).
   if (s->D > (1 << 26)) return fail(SDM_ERR_UNSUPPORTED, "D above 2^26");
   return SDM_OK;
 }
