@@ -15,7 +15,7 @@
 // Bound by memory: 16,384 rows of 2048 (bf16, bf16 residual and output) take 52
 // us, 5.1 TB/s; 16,384 rows of 4096 with an fp32 residual into codes with a scale
 // per row, and their decoding, 183 us for 0.94 GB, 5.1 TB/s; the gradient of
-// 32,768 rows of 2048 104 us, 5.2 TB/s.
+// 32,768 rows of 2048 88 us, 6.1 TB/s.
 #pragma once
 
 #include <type_traits>
@@ -422,11 +422,50 @@ struct NormGradArgs {
   float eps;
 };
 
+// Rows that a block walks (of whole 16-byte units) come through shared memory,
+// the next one on its way while a row is worked on: 88 us instead of 104 for
+// 32,768 rows of 2048 in bf16. (Registers for it cost the warps that hide the
+// rest, 115 us; the forward's kernels, with twice the warps, are slower this way,
+// 194 us instead of 181 for rows of 4096 into codes and back.) A thread copies
+// and reads its own values only, so that no barrier is needed; one 16-byte part
+// of one array lies side by side across the block's threads. kNormAheadBytes: a
+// thread's bytes of one array's row.
+template <typename T>
+constexpr int kNormAheadBytes = kNormV * 8 * static_cast<int>(sizeof(T));
+template <typename T, typename Tdy>
+constexpr int kNormGradRowBytes = 2 * kNormAheadBytes<T> + kNormAheadBytes<Tdy>;  // h, dh and dy
+template <typename T>
+__device__ __forceinline__ void norm_ahead(char* slot, const T* row, int t, int tpr, int d) {
+#pragma unroll
+  for (int j = 0; j < kNormV; ++j) {
+    const int c = norm_col<8>(j, 0, t, tpr);
+    if (c < d) {
+#pragma unroll
+      for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q)
+        cp_async16(slot + (j * (sizeof(T) / 2) + q) * tpr * 16 + t * 16, row + c + q * (16 / sizeof(T)));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void norm_arrived(const char* slot, int j, int t, int tpr, int d, float2* pairs) {
+  float v[8];
+  if (norm_col<8>(j, 0, t, tpr) < d) {
+#pragma unroll
+    for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q)
+      load_unit<T, 16 / sizeof(T)>(
+          reinterpret_cast<const T*>(slot + (j * (sizeof(T) / 2) + q) * tpr * 16 + t * 16), v + q * (16 / sizeof(T)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pairs[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+
 // With G = w dy: dx = dh + s G - h s^3 mean(G h), dw = sum over rows of dy h s.
 // One pass over the rows; a thread keeps the sums of its columns of dw over all
 // rows it meets in registers and writes them to its row group's slot, so dw is
 // the same on every run (k_sum_slots adds the slots in a fixed order).
-// All of a row's loads go out before the first sum.
 template <typename T, typename Tdy, bool kBlock, int kW>
 __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_residual_backward(const NormGradArgs a) {
   __shared__ float2 buf[2][32];
@@ -442,22 +481,44 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
   }
+  constexpr bool kAhead = kBlock && kW == 8;
+  extern __shared__ __align__(16) char ahead[];  // two rows of h, dy and dh
+  const int dy_at = kNormAheadBytes<T> * tpr, dh_at = dy_at + kNormAheadBytes<Tdy> * tpr;
+  auto slot = [&](int turn) { return ahead + turn * kNormGradRowBytes<T, Tdy> * tpr; };
+  auto fetch = [&](int64_t row, int turn) {
+    if (row < a.n_rows) {
+      norm_ahead(slot(turn), static_cast<const T*>(a.h) + row * d, t, tpr, d);
+      norm_ahead(slot(turn) + dy_at, static_cast<const Tdy*>(a.dy) + row * d, t, tpr, d);
+      if (a.dh != nullptr) norm_ahead(slot(turn) + dh_at, static_cast<const T*>(a.dh) + row * d, t, tpr, d);
+    }
+    cp_async_commit();
+  };
   int turn = 0;
+  if constexpr (kAhead) fetch(blockIdx.x, 0);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.n_rows;
        base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
     const int64_t row = base + group;
     const bool live = row < a.n_rows;
     const int64_t at = (live ? row : 0) * d;
+    if constexpr (kAhead) {
+      fetch(row + gridDim.x, turn ^ 1);
+      cp_async_wait<1>();
+    }
     float2 h[kNormV][4], g[kNormV][4], o[kNormV][4];
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) {
-      norm_load<T, kW>(static_cast<const T*>(a.h) + at, j, t, tpr, d, h[j]);
-      norm_load<Tdy, kW>(static_cast<const Tdy*>(a.dy) + at, j, t, tpr, d, g[j]);
-      if (a.dh != nullptr) {
-        norm_load<T, kW>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o[j]);
+      if constexpr (kAhead) {
+        norm_arrived<T>(slot(turn), j, t, tpr, d, h[j]);
+        norm_arrived<Tdy>(slot(turn) + dy_at, j, t, tpr, d, g[j]);
       } else {
+        norm_load<T, kW>(static_cast<const T*>(a.h) + at, j, t, tpr, d, h[j]);
+        norm_load<Tdy, kW>(static_cast<const Tdy*>(a.dy) + at, j, t, tpr, d, g[j]);
+      }
+      if (a.dh == nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = both(0.f);
+      } else if constexpr (!kAhead) {
+        norm_load<T, kW>(static_cast<const T*>(a.dh) + at, j, t, tpr, d, o[j]);
       }
     }
     float2 ss = both(0.f), dot = both(0.f);
@@ -474,6 +535,9 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
     const float s_acc = live ? s : 0.f;
 #pragma unroll
     for (int j = 0; j < kNormV; ++j) {
+      if constexpr (kAhead) {
+        if (a.dh != nullptr) norm_arrived<T>(slot(turn) + dh_at, j, t, tpr, d, o[j]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[j][i] = fma2(mul2(g[j][i], both(s_acc)), h[j][i], acc[j][i]);
@@ -483,9 +547,9 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
       if (live) norm_store<T, kW>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o[j]);
     }
   }
-  float* slot = a.part + (static_cast<int64_t>(blockIdx.x) * rpb + group) * d;
+  float* own = a.part + (static_cast<int64_t>(blockIdx.x) * rpb + group) * d;
 #pragma unroll
-  for (int j = 0; j < kNormV; ++j) norm_store<float, kW>(slot, j, t, tpr, d, acc[j]);
+  for (int j = 0; j < kNormV; ++j) norm_store<float, kW>(own, j, t, tpr, d, acc[j]);
 }
 
 // out[c] = sum over slots of part[slot, c], in a fixed order: 32 columns a

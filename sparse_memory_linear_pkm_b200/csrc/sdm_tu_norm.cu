@@ -45,7 +45,10 @@ unsigned norm_grid(const NormPlan& p, int64_t n_rows, int sms, int per_sm) {
   return static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(sms) * std::max(1, per_sm / p.threads)));
 }
 
-constexpr int kGradThreadsPerSm = 1024;
+// Threads of the gradient an SM holds at a time (127 registers): its blocks walk
+// the rows, as many as are resident.
+constexpr int kGradThreadsPerSm = 512;
+constexpr size_t kPlainSmem = 40 * 1024;  // dynamic shared memory beside a little static that needs no attribute
 
 sdm_status_t check_norm(int64_t n_rows, int32_t d, float eps) {
   if (n_rows < 0) return fail(SDM_ERR_INVALID_ARGUMENT, "n_rows must be >= 0");
@@ -85,8 +88,14 @@ void launch_norm_out(int out, const NormPlan& p, unsigned grid, const sdm::NormA
 
 template <typename T, typename Tdy, int kW>
 void launch_norm_grad_width(const NormPlan& p, unsigned grid, const sdm::NormGradArgs& a, cudaStream_t st) {
-  if (p.block) sdm::k_rmsnorm_residual_backward<T, Tdy, true, kW><<<grid, p.threads, 0, st>>>(a);
-  else sdm::k_rmsnorm_residual_backward<T, Tdy, false, kW><<<grid, p.threads, 0, st>>>(a);
+  if (p.block) {
+    const auto kern = sdm::k_rmsnorm_residual_backward<T, Tdy, true, kW>;
+    const size_t smem = kW == 8 ? 2 * sdm::kNormGradRowBytes<T, Tdy> * static_cast<size_t>(p.threads) : 0;
+    if (smem > kPlainSmem) set_smem(reinterpret_cast<const void*>(kern), smem);
+    kern<<<grid, p.threads, smem, st>>>(a);
+    return;
+  }
+  sdm::k_rmsnorm_residual_backward<T, Tdy, false, kW><<<grid, p.threads, 0, st>>>(a);
 }
 
 template <typename T, typename Tdy>
