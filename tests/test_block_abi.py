@@ -51,8 +51,8 @@ def test_norm_empty_and_sizes(lib):
     # 2 lanes a row of 32: 64 rows a block, a slot of d sums each
     assert size(4, 32) == 64 * 32 * 4
     assert size(1, 2048) == 2048 * 4 and size(3, 2048) == 3 * 2048 * 4
-    # at most 1024 threads' worth of blocks on each of 148 SMs
-    assert size(1 << 20, 2048) == 148 * 8 * 2048 * 4
+    # at most 512 threads' worth of blocks on each of 148 SMs
+    assert size(1 << 20, 2048) == 148 * 4 * 2048 * 4
     args = [P, native.F32, P, native.F32, P, native.F32, None, 3, 2048, 1e-6, P, P, P, size(3, 2048) - 1, None]
     refused(lib, lib.sdm_rmsnorm_residual_backward(*args), "workspace")
     args[12] = None
