@@ -159,7 +159,7 @@ def test_scan_refuses_pointers(lib):
     # few channels, many tokens: two arrays of states before the splits
     long = shape(B=1, T=8192, D=32)
     need = lib.sdm_selective_scan_workspace_bytes(ctypes.byref(long))
-    assert need == 2 * 64 * 32 * 16 * 4  # 64 splits of 128 tokens
+    assert need == 2 * 256 * 32 * 16 * 4  # 256 splits of 32 tokens
     refused(lib, lib.sdm_selective_scan(ctypes.byref(long), *([P] * 12), P, need - 1, None), "workspace is smaller")
     refused(lib, lib.sdm_selective_scan(ctypes.byref(long), *([P] * 12), None, need, None), "workspace is NULL")
     assert lib.sdm_selective_scan_workspace_bytes(s) == 0
