@@ -162,8 +162,9 @@ static __global__ void __launch_bounds__(kClipThreads, kClipPerSm) k_grad_clip(c
   double acc = 0.0;
   for (int i = threadIdx.x; i < n_slots; i += kClipThreads) acc += slots[i];
   const double norm = sqrt(block_sum64(acc, buf));
+  // A ratio that is not a number stays one, but for an infinite max_norm: that scales nothing, whatever the norm is.
   const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
-  const float c = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);  // not a number stays one
+  const float c = ratio > 1.0 || isinf(max_norm) ? 1.0f : static_cast<float>(ratio);
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
   const int chunks = t.first[t.tensors];
   for (int r = blockIdx.x; r < chunks; r += gridDim.x) {

@@ -92,6 +92,23 @@ def test_not_finite(sdm):
     assert math.isnan(float(sdm.grad_norm_clip([g], 1.0, out=[out]))) and bool(torch.isnan(out).all())
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype,out_dtype", [(F32, F32), (F32, BF16), (BF16, F32)])
+def test_infinite_max_norm_copies_whatever_the_norm_is(sdm, value, dtype, out_dtype):
+    """max_norm = inf scales nothing: a gradient that is not finite leaves all other values as they are."""
+    g = torch.randn(5000, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    g[77] = value
+    rest = torch.randn(301, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    outs = [torch.empty(t.shape, dtype=out_dtype, device="cuda") for t in (g, rest)]
+    norm = sdm.grad_norm_clip([g, rest], float("inf"), out=outs)
+    assert not math.isfinite(float(norm))
+    for got, want in zip(outs, (g, rest)):
+        assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(want.to(out_dtype), nan=7.0))
+    before = g.clone()
+    sdm.grad_norm_clip([g, rest], float("inf"))
+    assert torch.equal(torch.nan_to_num(g, nan=7.0), torch.nan_to_num(before, nan=7.0))
+
+
 def test_same_bits_every_time(sdm):
     g = [torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda() for n in (1_000_003, 77, 250_000)]
     first = sdm.grad_norm_clip(g, float("inf"))
