@@ -1,0 +1,31 @@
+"""The operators around the recurrent core at the ends of their ranges and in
+the launch shapes that large calls take."""
+
+import pytest
+import torch
+
+pytestmark = [pytest.mark.gpu, pytest.mark.slow]
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def small_integers(n: int) -> torch.Tensor:
+    """n values 1 .. 8 in bf16, of a fixed seed, made on the device in parts."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    out = torch.empty(n, dtype=BF16, device="cuda")
+    for part in out.split(1 << 28):
+        part.copy_(torch.randint(1, 9, part.shape, generator=g, device="cuda", dtype=torch.int8))
+    return out
+
+
+def test_longest_sequence_of_the_scan(sdm):
+    """The most tokens that a call takes, one channel: the last split's end, rounded up to whole tiles, lies above
+    2^31. With steps of 1 and A = -60 nothing outlasts its token (e^-60 of it is left), so y is x, exactly."""
+    T = 2 ** 31 - 1 - 4096
+    x, one = small_integers(T).view(1, T, 1), torch.ones(T, dtype=BF16, device="cuda")
+    state = torch.zeros(1, 1, 1, device="cuda")
+    y = torch.zeros_like(x)
+    sdm.selective_scan(x, one.view(1, T, 1), torch.full((1, 1), -60.0, device="cuda"), one.view(1, T, 1, 1),
+                       one.view(1, T, 1, 1), softplus=False, state=state, y=y)
+    assert torch.equal(y, x)
+    assert float(state) == float(x[0, -1, 0])
+    sdm.stream_check()
