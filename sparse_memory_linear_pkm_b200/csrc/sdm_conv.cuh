@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256) k_short_conv(const ConvArgs a) {
   conv_weights<K, V>(a.w, a.w_bf16, a.w_whole, c0, n, w);
   conv_bias<V>(a.bias, a.w_bf16, c0, n, bias);
   const int len = clamp_length(a.lengths, b, a.T, a.err);
-  const int t1 = min(len, t0 + a.run);
+  const int t1 = min(len, t0 + min(a.run, a.T - t0));  // (t0 + run may pass 2^31)
   if (t0 >= len && run != 0) return;
 
   RawUnit<T, V> old[K - 1], next[kConvAhead];

@@ -29,3 +29,21 @@ def test_longest_sequence_of_the_scan(sdm):
     assert torch.equal(y, x)
     assert float(state) == float(x[0, -1, 0])
     sdm.stream_check()
+
+
+@pytest.mark.parametrize("K", [2, 8])
+def test_longest_sequence_of_the_convolution(sdm, K):
+    """The most tokens that a call takes: the last run's end lies above 2^31. The last tap alone gives y = x, the first
+    alone the input K - 1 tokens before."""
+    T = 2 ** 31 - 17
+    x = small_integers(T).view(1, T, 1)
+    state = torch.full((1, K - 1, 1), 9.0, dtype=BF16, device="cuda")
+    y = torch.zeros_like(x)
+    w = torch.zeros(1, K, device="cuda")
+    w[0, K - 1] = 1.0
+    sdm.short_conv(x, w, silu=False, state=state, y=y)
+    assert torch.equal(y, x) and torch.equal(state, x[:, T - K + 1:])
+    state.fill_(9.0)
+    sdm.short_conv(x, w.flip(1).contiguous(), silu=False, state=state, y=y)
+    assert torch.equal(y[:, K - 1:], x[:, :T - K + 1]) and bool((y[:, :K - 1] == 9.0).all())
+    sdm.stream_check()
