@@ -201,8 +201,9 @@ __device__ __forceinline__ uint2 norm_fp8blk(const float2* h, const float2* w, d
     mx = fmaxf(mx, fmaxf(fabsf(u[i].x), fabsf(u[i].y)));
   }
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  // mx = f 2^k, f in [0.5, 1); the ends of fp32's range, and zeros, go the 64-bit way.
-  bool sure = mx > 1e-30f && mx < 3e38f;
+  // mx = f 2^k, f in [0.5, 1); the ends of fp32's range, and zeros, go the 64-bit way: those of h w too (mx / s),
+  // where products below the normal range have lost bits that a large s brings up.
+  bool sure = mx > 1e-30f * fmaxf(sf.x, 1.0f) && mx < 3e38f;
   const uint32_t bits = __float_as_uint(mx);
   const float f = __uint_as_float((bits & 0x007FFFFFu) | 0x3F000000u);
   int e = sure ? fp8blk_exponent(f > 0.90625f, static_cast<int>(bits >> 23) - 126) : 0;

@@ -88,6 +88,27 @@ def test_codes_of_odd_rows(sdm):
     assert torch.equal(strip(got.view(torch.uint8).cpu()), strip(codes))
 
 
+@pytest.mark.parametrize("d", [64, 2048])
+@pytest.mark.parametrize("scale,w_scale,eps", [(1e-38, 0.01, 0.0), (1e-30, 1e-12, 0.0), (1e-25, 1e-16, 1e-55),
+                                               (1e-42, 1.0, 0.0), (1e-20, 1e-22, 1e-44)])
+def test_codes_of_products_below_the_normal_range(sdm, d, scale, w_scale, eps):
+    """h w leaves fp32's normal range and a large s brings it back: the codes are still those of the real values."""
+    g = torch.Generator().manual_seed(d)
+    x = (torch.randn(40, d, generator=g).double() * scale).float().cuda()
+    w = ((torch.rand(d, generator=g).double() + 0.5) * w_scale).float().cuda()
+    eps = float(torch.tensor(eps, dtype=torch.float32))  # as the call takes it
+    want, _ = ref.norm(x, w, None, eps)
+    strip = lambda c: torch.where(c == 128, 0, c)  # noqa: E731  (the sign of a zero is not kept by every rounding)
+    buf, _ = sdm.rmsnorm_residual(x, w, None, out="fp8blk", eps=eps)
+    codes, exps = ref.fp8blk(want)
+    assert torch.equal(buf[40 * d:].cpu().view(torch.int8), exps)
+    assert torch.equal(strip(buf[:40 * d].cpu().reshape(40, d)), strip(codes))
+    (got, scales), _ = sdm.rmsnorm_residual(x, w, None, out="fp8row", eps=eps)
+    codes, c = ref.fp8row(want)
+    assert torch.equal(scales.cpu(), c)
+    assert torch.equal(strip(got.view(torch.uint8).cpu()), strip(codes))
+
+
 @pytest.mark.parametrize("out", ["f32", "fp8blk", "fp8row"])
 def test_not_a_number_stays_in_its_row(sdm, out):
     xs, w, _ = make(3, 48, F32, None)
