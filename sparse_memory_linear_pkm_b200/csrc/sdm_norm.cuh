@@ -89,6 +89,10 @@ struct OpSum {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
   __device__ __forceinline__ float over(float v, int o) const { return v + __shfl_xor_sync(0xffffffffu, v, o); }
 };
+struct OpMax {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+  __device__ __forceinline__ float over(float v, int o) const { return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o)); }
+};
 struct OpSum2 {
   __device__ __forceinline__ float2 operator()(float2 a, float2 b) const { return add2(a, b); }
   __device__ __forceinline__ float2 over(float2 v, int o) const {
@@ -125,6 +129,28 @@ __device__ __forceinline__ T row_reduce(T v, int tpr, T* buf, Op op) {
     for (int i = 1; i < warps; ++i) v = op(v, buf[i]);
   }
   return v;
+}
+
+// Brings a row with `wide` set whose squares do not fit fp32 into its middle: h
+// becomes h k for the returned power of two k by which the larger of max |h| and
+// sqrt(eps) is in [1, 2) (or next to it, at the ends of fp32's range); the mean
+// square with eps is then k^2 times what it was. k = 1 for other rows. Every
+// thread of the row's block or warp calls it.
+template <bool kBlock>
+__device__ __forceinline__ float norm_rescale(float2 (&h)[kNormV][4], bool wide, float eps, int tpr, float* buf) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < kNormV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(h[j][i].x), fabsf(h[j][i].y)));
+  m = fmaxf(row_reduce<kBlock>(m, tpr, buf, OpMax()), sqrtf(eps));
+  const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  const float k = wide ? pow2f(-min(126, max(-126, e))) : 1.0f;
+#pragma unroll
+  for (int j = 0; j < kNormV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[j][i] = mul2(h[j][i], both(k));
+  return k;
 }
 
 // 1 / sqrt(v) in 64 bits: two Newton steps from the fp32 value where v is in
@@ -255,7 +281,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
     k_rmsnorm_residual(const NormArgs a) {
   constexpr bool k8bit = kOut >= kNormFp8Blk;
   __shared__ SumMax buf64[k8bit ? 2 : 1][k8bit ? 32 : 1];
-  __shared__ float buf32[k8bit ? 1 : 2][k8bit ? 1 : 32];
+  __shared__ float buf32[k8bit ? 1 : 4][k8bit ? 1 : 32];  // two in turn, and two for rows that are scaled
   __shared__ unsigned long long s_max[2];
   const int d = a.d, tpr = a.tpr;
   const int t = kBlock ? threadIdx.x : threadIdx.x & (tpr - 1);
@@ -296,8 +322,19 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
       for (int j = 0; j < kNormV; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss = fma2(h[j][i], h[j][i], ss);
-      const float sum = row_reduce<kBlock>(ss.x + ss.y, tpr, buf32[turn], OpSum());
-      const float s = 1.0f / sqrtf(sum / static_cast<float>(d) + a.eps);
+      float mean = row_reduce<kBlock>(ss.x + ss.y, tpr, buf32[turn], OpSum()) / static_cast<float>(d) + a.eps;
+      // Below, squares have left fp32's normal range; above, their sum may have. (Threads of a block hold one mean.)
+      const bool wide = mean < 1e-34f || mean > 1e34f;
+      if (kBlock ? wide : __any_sync(0xffffffffu, wide)) {
+        const float k = norm_rescale<kBlock>(h, wide, a.eps, tpr, buf32[2]);
+        ss = both(0.f);
+#pragma unroll
+        for (int j = 0; j < kNormV; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = fma2(h[j][i], h[j][i], ss);
+        mean = row_reduce<kBlock>(ss.x + ss.y, tpr, buf32[3], OpSum()) / static_cast<float>(d) + a.eps * k * k;
+      }
+      const float s = 1.0f / sqrtf(mean);
       using Ty = std::conditional_t<kOut == kNormF32, float, bf16>;
 #pragma unroll
       for (int j = 0; j < kNormV; ++j) {

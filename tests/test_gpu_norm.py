@@ -142,6 +142,47 @@ def test_decoding(sdm, dtype):
     assert sdm.dequantize_fp8blk(state, xs.shape).shape == xs.shape
 
 
+def rows_of_scales(d, dtype, seed=0):
+    """Rows whose squares leave fp32's range and rows that do not, side by side."""
+    scales = [1e-44, 1e-42, 1e-38, 1.0, 1e-30, 1e-25, 3e-21, 1e-19, 1e-18, 1e-16, 3e15, 1e17, 1e20, 2.0, 1e30, 3e37]
+    g = torch.Generator().manual_seed(seed + d)
+    x = torch.randn(len(scales), d, generator=g).double().clamp(-4, 4) * torch.tensor(scales).double()[:, None]
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("d", [1, 7, 24, 128, 512, 600, 1000, 2048, 8191])
+@pytest.mark.parametrize("dtype,eps", [(F32, 0.0), (F32, 1e-42), (F32, 1e-36), (F32, 1e30), (BF16, 0.0), (BF16, 1e-6)])
+def test_rows_whose_squares_leave_the_range(sdm, d, dtype, eps):
+    """Scaling by a power of two is exact, so the errors are those of other rows. (A row that rounded to zeros has no
+    norm with eps = 0: not a number, as the definition.)"""
+    x = rows_of_scales(d, dtype)
+    w = (torch.rand(d, generator=torch.Generator().manual_seed(d)) + 0.5).cuda()
+    eps = float(torch.tensor(eps, dtype=torch.float32))  # as the call takes it
+    want, _ = ref.norm(x, w, None, eps)
+    y, _ = sdm.rmsnorm_residual(x, w, None, out="f32", eps=eps)
+    none = torch.isnan(want)
+    assert torch.equal(torch.isnan(y.cpu()), none)
+    want = torch.where(none, 0.0, want)
+    # Below fp32's normal range (rows far below sqrt(eps)) roundings are absolute, half the least step of 2^-149 each:
+    # that of h s, which w <= 1.5 multiplies, and that of its product with w: (1.5 + 1) 2^-150.
+    ref.assert_within(torch.nan_to_num(y), want, NORM_REL * want.abs() + 2.5 * 2.0 ** -150, "y")
+
+
+def test_infinite_values_of_a_row(sdm):
+    """s is 0: 0 for finite values and not a number for infinite ones, and rows beside it keep their bits."""
+    x = rows_of_scales(64, F32)
+    w = torch.ones(64, device="cuda")
+    clean = sdm.rmsnorm_residual(x, w, None, eps=0.0)[0]
+    x[3, 5] = float("inf")
+    x[13, 9] = float("-inf")
+    y = sdm.rmsnorm_residual(x, w, None, eps=0.0)[0]
+    for r in range(16):
+        if r in (3, 13):
+            assert bool((torch.isnan(y[r]) == torch.isinf(x[r])).all()) and not torch.nan_to_num(y[r]).any()
+        else:
+            assert torch.equal(y[r], clean[r])
+
+
 def test_in_place_residual_and_output(sdm):
     xs, w, r = make(9, 640, BF16, BF16, seed=4)
     y, h = sdm.rmsnorm_residual(xs, w, r)
