@@ -485,10 +485,9 @@ SDM_API sdm_status_t sdm_layer_forward_noalloc(const sdm_shape_t* shape, const v
  *   y may be x itself where the types agree. d in [1, 8192]; rows that are a
  *   multiple of 8 values are moved in 16-byte units. scales: as above, NULL
  *   for the other types. The sum of squares is held in 64 bits for the 8-bit
- *   types and in fp32 for the others; a row whose squares leave fp32's range
- *   (tiny ones with eps near 0, huge ones) is first brought into it by a power
- *   of two. The gradient asks for |h| below 1e17 and, where eps is below 1e-20,
- *   for rows whose mean square is above that. */
+ *   types and in fp32 for the others and the gradient; a row whose squares leave
+ *   fp32's range (tiny ones with eps near 0, huge ones) is first brought into it
+ *   by a power of two. */
 SDM_API sdm_status_t sdm_rmsnorm_residual(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype,
                                   const void* w, int32_t w_dtype, int64_t n_rows, int32_t d, float eps, void* h,
                                   void* y, int32_t y_dtype, void* scales, void* stream);

@@ -506,7 +506,8 @@ __device__ __forceinline__ void norm_arrived(const char* slot, int j, int t, int
 // the same on every run (k_sum_slots adds the slots in a fixed order).
 template <typename T, typename Tdy, bool kBlock, int kW>
 __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_residual_backward(const NormGradArgs a) {
-  __shared__ float2 buf[2][32];
+  __shared__ float2 buf[3][32];  // two in turn, and one for rows that are scaled
+  __shared__ float buf_max[32];
   const int d = a.d, tpr = a.tpr;
   const int t = kBlock ? threadIdx.x : threadIdx.x & (tpr - 1);
   const int rpb = kBlock ? 1 : blockDim.x / tpr;
@@ -567,8 +568,24 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
         ss = fma2(h[j][i], h[j][i], ss);
         dot = fma2(mul2(g[j][i], w[j][i]), h[j][i], dot);
       }
-    const float2 sums = row_reduce<kBlock>(make_float2(ss.x + ss.y, dot.x + dot.y), tpr, buf[turn], OpSum2());
-    const float s = 1.0f / sqrtf(sums.x / static_cast<float>(d) + a.eps);
+    float2 sums = row_reduce<kBlock>(make_float2(ss.x + ss.y, dot.x + dot.y), tpr, buf[turn], OpSum2());
+    float mean = sums.x / static_cast<float>(d) + a.eps, k = 1.0f;
+    // Beyond, s^3 mean(G h) or the squares leave fp32's range for ordinary G: as in the forward, h k takes h's place.
+    const bool wide = mean < 1e-20f || mean > 1e20f;
+    if (kBlock ? wide : __any_sync(0xffffffffu, wide)) {
+      k = norm_rescale<kBlock>(h, wide, a.eps, tpr, buf_max);
+      ss = dot = both(0.f);
+#pragma unroll
+      for (int j = 0; j < kNormV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ss = fma2(h[j][i], h[j][i], ss);
+          dot = fma2(mul2(g[j][i], w[j][i]), h[j][i], dot);
+        }
+      sums = row_reduce<kBlock>(make_float2(ss.x + ss.y, dot.x + dot.y), tpr, buf[2], OpSum2());
+      mean = sums.x / static_cast<float>(d) + a.eps * k * k;
+    }
+    const float s = 1.0f / sqrtf(mean);
     const float corr = sums.y / static_cast<float>(d) * s * s * s;
     const float s_acc = live ? s : 0.f;
 #pragma unroll
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, 1) k_rmsnorm_r
       for (int i = 0; i < 4; ++i) {
         acc[j][i] = fma2(mul2(g[j][i], both(s_acc)), h[j][i], acc[j][i]);
         const float2 own = fma2(h[j][i], both(-corr), mul2(mul2(g[j][i], w[j][i]), both(s)));
-        o[j][i] = add2(o[j][i], own);
+        o[j][i] = fma2(own, both(k), o[j][i]);
       }
       if (live) norm_store<T, kW>(static_cast<T*>(a.dx) + at, j, t, tpr, d, o[j]);
     }

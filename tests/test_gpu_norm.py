@@ -218,6 +218,32 @@ def test_gradient(sdm, rows, d, h, dy, with_dh):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("d", [1, 7, 24, 512, 600, 2048])
+@pytest.mark.parametrize("dtype,eps", [(F32, 0.0), (F32, 1e-40), (F32, 1e-6), (BF16, 0.0), (BF16, 1e25)])
+def test_gradient_of_rows_whose_squares_leave_the_range(sdm, d, dtype, eps):
+    scales = [1e-36, 1.0, 1e-30, 1e-25, 1e-21, 3e-19, 1e-15, 1e-10, 1e-9, 1e10, 1e12, 1e17, 1e20, 2.0, 1e30, 3e37]
+    g = torch.Generator().manual_seed(d)
+    h = (torch.randn(16, d, generator=g).double().clamp(-4, 4) * torch.tensor(scales).double()[:, None]).to(dtype).cuda()
+    w = (torch.rand(d, generator=g) + 0.5).cuda()
+    dy, dh = (torch.randn(16, d, generator=g).to(dtype).cuda() for _ in range(2))
+    eps = float(torch.tensor(eps, dtype=torch.float32))  # as the call takes it
+    hh, ww = ref.d(h).requires_grad_(), ref.d(w).requires_grad_()
+    y = hh / torch.sqrt((hh * hh).mean(-1, keepdim=True) + eps) * ww
+    wdx, wdw = torch.autograd.grad((y * ref.d(dy)).sum() + (hh * ref.d(dh)).sum(), [hh, ww])
+    alone = torch.autograd.grad((hh / torch.sqrt((hh * hh).mean(-1, keepdim=True) + eps) * ww * ref.d(dy)).sum(), hh)[0]
+    H, G = ref.d(h).abs(), (ref.d(dy) * ref.d(w)).abs()
+    s = 1 / torch.sqrt((H * H).mean(-1, keepdim=True) + eps)
+    size = G * s + H * s ** 3 * (G * H).mean(-1, keepdim=True)
+    dx, dw = sdm.rmsnorm_residual_backward(h, w, dy, dh, eps=eps)
+    ref.assert_within(dx, wdx, 110 * ref.U * (size + ref.d(dh).abs()), "dx")  # as for other rows
+    adds = 1 + 40 + 32
+    ref.assert_within(dw, wdw, (adds + 24) * ref.U * (ref.d(dy).abs() * H * s).sum(0), "dw")
+    # without dh: below the type's normal range the fp32 value and its rounding are off by half a least step each
+    least = 2.0 ** -149 if dtype == F32 else 2.0 ** -133
+    dx, _ = sdm.rmsnorm_residual_backward(h, w, dy, None, eps=eps)
+    ref.assert_within(dx, alone, 110 * ref.U * size + 2.0 ** -150 + least / 2, "dx without dh")
+
+
 def test_gradient_against_differences(sdm):
     """The loss' change along a direction, from 64-bit forward passes, is the gradient's product with it."""
     hs, w, _ = make(6, 40, F32, None, seed=8)
