@@ -572,7 +572,9 @@ SDM_API size_t sdm_selective_scan_workspace_bytes(const sdm_selscan_shape_t* sha
  *   A [D,N], Dskip [D] or NULL, dt_bias [D] or NULL: fp32. A is finite and, for
  *     a state that decays, negative. Long sequences are computed in parts, each
  *     part's decays as one factor: where delta A sums to more than 88 in a part
- *     (growing states), that factor, and what it multiplies, is not finite.
+ *     (growing states), that factor, and what it multiplies, is not finite. A
+ *     state that is infinite stays so, however far its decays go; a y that it
+ *     reaches is not finite (an infinity may come out as not a number).
  *   lengths [B] int32 or NULL, as in sdm_short_conv
  *   h0 [B,D,N] fp32 or NULL (zeros): the state before the first token;
  *   hT [B,D,N] fp32 or NULL: the state after each row's last token; may be h0,
@@ -593,7 +595,9 @@ SDM_API size_t sdm_selective_scan_backward_workspace_bytes(const sdm_selscan_sha
  *   dx, ddt, dz (with z) [B,T,D], dB, dC [B,T,G,N]: in_dtype, contiguous, 0 for
  *   tokens past a row's length; dA [D,N], dD [D], ddt_bias [D] fp32 (the last
  *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL. Outputs
- *   must not overlap inputs. Deterministic. */
+ *   must not overlap inputs. What an infinite state or derivative reaches is not
+ *   finite (an infinity of the formulas may come out as not a number).
+ *   Deterministic. */
 SDM_API sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const void* x, const void* dt,
                                          const float* A, const void* Bm, const void* Cm, const float* Dskip,
                                          const void* z, const float* dt_bias, const int32_t* lengths,

@@ -356,6 +356,13 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan(const SelScanArg
   }
 }
 
+// A split's map P h + H of a state. A decay over the whole split that came out as
+// 0 is still a positive factor: it leaves an infinite state infinite, as the
+// tokens one by one do.
+__device__ __forceinline__ float join_states(float P, float h, float H) {
+  return P == 0.0f && isinf(h) ? h + H : fmaf(P, h, H);
+}
+
 // States before each split from the splits' maps, in place of their H parts:
 // a thread per (b, d, n) walks the splits in order.
 static __global__ void __launch_bounds__(256) k_selective_scan_join(const float* __restrict__ P, float* H,
@@ -387,7 +394,7 @@ static __global__ void __launch_bounds__(256) k_selective_scan_join(const float*
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (s0 + j < splits) H[at + j * per_b] = h;
-      h = fmaf(p0[j], h, q0[j]);
+      h = join_states(p0[j], h, q0[j]);
     }
   }
 }

@@ -148,6 +148,32 @@ def test_far_step_sizes(sdm):
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(v["state"]).all())
 
 
+@pytest.mark.parametrize("N", [4, 16, 24, 64])
+@pytest.mark.parametrize("where", ["input", "state"])
+def test_infinite_state_outlasts_its_decay(sdm, N, where):
+    """An infinite state of one channel stays infinite with its sign over splits whose decay is 0 in fp32, as token by
+    token (no token's own decay is 0 here); other channels keep their bits."""
+    v = make(1, 700, 20, N, 2, seed=N)
+    v["dt_bias"] = v["dt_bias"] + 3  # some 50 of delta a split: e^(-4 * 50) is 0 in fp32
+    clean = dict(v, state=v["state"].clone())
+    clean_y = call(sdm, clean)
+    if where == "input":
+        v["x"][0, 60, 5] = float("inf")
+    else:
+        v["state"][0, 5] = torch.where(torch.arange(N, device="cuda") % 2 == 0, float("inf"), float("-inf"))
+    w = wide(v)
+    delta = torch.log1p(torch.exp(w["dt"] + w["dt_bias"]))
+    assert float((delta[..., None] * w["A"]).min()) > -80 and float((delta[:, 96:144, 5, None] * w["A"][5]).sum(1).min()) < -110
+    want, h = ref.scan(**w)
+    assert bool(torch.isinf(h[0, 5]).all())
+    y = call(sdm, v)
+    assert torch.equal(ref.d(v["state"])[0, 5], h[0, 5])
+    # which of infinity and not a number y is there is not said: states that pad N make 0 * inf of it
+    assert torch.equal(torch.isfinite(ref.d(y)), torch.isfinite(want))
+    rest = [c for c in range(20) if c != 5]
+    assert torch.equal(y[..., rest], clean_y[..., rest]) and torch.equal(v["state"][:, rest], clean["state"][:, rest])
+
+
 GRAD_SIZES = [(1, 1, 1, 1, 1), (2, 3, 8, 16, 1), (1, 9, 5, 3, 1), (2, 20, 6, 7, 2), (1, 64, 33, 16, 1),
               (2, 65, 24, 32, 2), (1, 130, 20, 64, 4), (2, 70, 140, 16, 1), (3, 200, 9, 8, 3)]
 
