@@ -60,10 +60,11 @@ struct SelScanArgs {
   unsigned* err;
 };
 
-// First token behind the split that begins at t_begin <= T. (t_begin +
-// tokens_per_split itself may lie above 2^31: whole tiles reach past T.)
-__device__ __forceinline__ int split_stop(const SelScanArgs& a, int t_begin) {
-  return t_begin + min(a.tokens_per_split, a.T - t_begin);
+// First token behind the split that begins at t_begin, of the `len` there are.
+// (Whole tiles reach past T, so that the sum may lie above 2^31.)
+__device__ __forceinline__ int split_stop(const SelScanArgs& a, int t_begin, int len) {
+  return static_cast<int>(
+      min(static_cast<unsigned>(len), static_cast<unsigned>(t_begin) + static_cast<unsigned>(a.tokens_per_split)));
 }
 
 enum SelMode { kSelRun = 0, kSelSums = 1 };
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kSelThreads) k_selective_scan(const SelScanArg
   const int Dg = a.D / a.G, c_end = (group + 1) * Dg;
   const int len = clamp_length(a.lengths, b, a.T, a.err);
   const int t_begin = split * a.tokens_per_split;
-  const int t_end = min(len, split_stop(a, t_begin));
+  const int t_end = split_stop(a, t_begin, len);
 
   // This lane's channel (the last one again where there is none) and states.
   const int c_want = group * Dg + tile_c * CH + tid / L, c = min(c_want, c_end - 1);

@@ -72,7 +72,7 @@ __device__ __forceinline__ SelPlace sel_place(const SelScanArgs& a) {
   p.live = c < (p.group + 1) * Dg;
   p.c = min(c, (p.group + 1) * Dg - 1);
   p.t_begin = p.split * a.tokens_per_split;
-  p.t_stop = split_stop(a, p.t_begin);
+  p.t_stop = split_stop(a, p.t_begin, a.T);
   p.t_end = min(clamp_length(a.lengths, p.b, a.T, a.err), p.t_stop);
   return p;
 }
