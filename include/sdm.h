@@ -594,8 +594,9 @@ SDM_API size_t sdm_selective_scan_backward_workspace_bytes(const sdm_selscan_sha
  * the workspace).
  *   dx, ddt, dz (with z) [B,T,D], dB, dC [B,T,G,N]: in_dtype, contiguous, 0 for
  *   tokens past a row's length; dA [D,N], dD [D], ddt_bias [D] fp32 (the last
- *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL. Outputs
- *   must not overlap inputs. What an infinite state or derivative reaches is not
+ *   two may be NULL without Dskip / dt_bias); dh0 [B,D,N] fp32 or NULL; may be
+ *   dhT. But for that, outputs must not overlap an input or one another
+ *   (refused). What an infinite state or derivative reaches is not
  *   finite (an infinity of the formulas may come out as not a number).
  *   Deterministic. */
 SDM_API sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const void* x, const void* dt,

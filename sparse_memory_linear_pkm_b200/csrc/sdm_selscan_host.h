@@ -29,9 +29,10 @@ sdm_status_t need_selscan(const sdm_selscan_shape_t& s, bool any, const void* x,
                           const void* Bm, const void* Cm, const float* Dskip, const void* z, const float* dt_bias,
                           const int32_t* lengths);
 
-// The memory that a call's token inputs take, for check_apart: x, dt, z, B, C.
+// The memory that a call's inputs take, for check_apart: x, dt, z, B, C, A, Dskip, dt_bias, lengths.
+constexpr int kSelInputs = 9;
 struct SelInputs {
-  Piece piece[5];
+  Piece piece[kSelInputs];
 };
 SelInputs selscan_inputs(const sdm_selscan_shape_t& s, const sdm::SelScanArgs& a);
 

@@ -145,7 +145,11 @@ SelInputs selscan_inputs(const sdm_selscan_shape_t& s, const sdm::SelScanArgs& a
            {"dt", a.dt, (last * a.dt_stride + d) * es},
            {"z", a.z, (last * a.z_stride + d) * es},
            {"Bm", a.Bm, (last * a.b_stride + gn) * es},
-           {"Cm", a.Cm, (last * a.c_stride + gn) * es}}};
+           {"Cm", a.Cm, (last * a.c_stride + gn) * es},
+           {"A", a.A, d * s.N * sizeof(float)},
+           {"Dskip", a.Dskip, d * sizeof(float)},
+           {"dt_bias", a.bias, d * sizeof(float)},
+           {"lengths", a.lengths, s.B * sizeof(int32_t)}}};
 }
 
 // The pointers that the scan and its gradient share.
@@ -209,7 +213,7 @@ sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x,
   const size_t states = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
   const Piece outs[] = {{"y", y, static_cast<size_t>(s.B) * s.T * s.D * in_size(s.in_dtype)}, {"hT", hT, states}};
   const Piece start = {"h0", hT == h0 ? nullptr : h0, states};
-  if ((r = check_apart(outs, 2, in.piece, 5)) || (r = check_apart(outs, 2, &start, 1))) return r;
+  if ((r = check_apart(outs, 2, in.piece, kSelInputs)) || (r = check_apart(outs, 2, &start, 1))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
   a.err = dev->err;

@@ -136,10 +136,12 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   const SelInputs in = selscan_inputs(s, a.f);
   const size_t es = in_size(s.in_dtype), tokens = static_cast<size_t>(s.B) * s.T, rows = tokens * s.D * es;
   const size_t bc = tokens * s.G * s.N * es;
-  const Piece more[] = {{"dy", dy, rows}, {"h0", h0, states}};
-  const Piece outs[] = {{"dx", dx, rows}, {"ddt", ddt, rows}, {"dz", dz, rows}, {"dB", dB, bc},
-                        {"dC", dC, bc},   {"dA", dA, static_cast<size_t>(s.D) * s.N * sizeof(float)}};
-  if ((r = check_apart(outs, 6, in.piece, 5)) || (r = check_apart(outs, 6, more, 2))) return r;
+  const size_t row = s.D * sizeof(float);
+  // (dh0 may be dhT: one thread reads a value of dhT and writes that of dh0.)
+  const Piece more[] = {{"dy", dy, rows}, {"h0", h0, states}, {"dhT", dhT == dh0 ? nullptr : dhT, states}};
+  const Piece outs[] = {{"dx", dx, rows}, {"ddt", ddt, rows}, {"dz", dz, rows},  {"dB", dB, bc},  {"dC", dC, bc},
+                        {"dA", dA, row * s.N}, {"dD", dD, row}, {"ddt_bias", ddt_bias, row}, {"dh0", dh0, states}};
+  if ((r = check_apart(outs, 9, in.piece, kSelInputs)) || (r = check_apart(outs, 9, more, 3))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
   a.f.err = dev->err;

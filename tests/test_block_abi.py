@@ -186,6 +186,33 @@ def test_scan_gradient_refuses(lib):
         refused(lib, lib.sdm_selective_scan_backward(ctypes.byref(s), *args, need, None), f"{names[i]} overlaps {names[j]}")
 
 
+def test_scan_refuses_outputs_on_any_input(lib):
+    """Parameters, lengths and states count as inputs too, and every output as one."""
+    s = shape()
+    names = ["x", "dt", "A", "Bm", "Cm", "Dskip", "z", "dt_bias", "lengths", "h0", "hT", "y"]
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(22)]
+    for i in (10, 11):
+        for j in (2, 5, 7, 8):
+            args = far[:12]
+            args[i] = far[j]
+            refused(lib, lib.sdm_selective_scan(ctypes.byref(s), *args, None, 0, None), f"{names[i]} overlaps {names[j]}")
+    need = lib.sdm_selective_scan_backward_workspace_bytes(ctypes.byref(s))
+    names = ["x", "dt", "A", "Bm", "Cm", "Dskip", "z", "dt_bias", "lengths", "h0", "dy", "dhT", "dx", "ddt", "dA", "dB",
+             "dC", "dD", "dz", "ddt_bias", "dh0"]
+    for i in range(12, 21):
+        for j in range(12):
+            args = list(far)
+            args[i] = ctypes.c_void_p(far[j].value + (16 if (i, j) == (20, 11) else 0))
+            refused(lib, lib.sdm_selective_scan_backward(ctypes.byref(s), *args, need, None),
+                    f"{names[i]} overlaps {names[j]}")
+        for j in range(12, 21):
+            if i != j:
+                args = list(far)
+                args[i] = far[j]
+                status = lib.sdm_selective_scan_backward(ctypes.byref(s), *args, need, None)
+                assert status == 1 and b" overlaps " in lib.sdm_last_error()
+
+
 def clip(lib, entries, max_norm=1.0, eps=1e-6, norm=P, ws=P, ws_bytes=None):
     table = (native.GradTensor * max(1, len(entries)))(*[native.GradTensor(*e) for e in entries])
     n = lib.sdm_grad_norm_clip_workspace_bytes(len(entries)) if ws_bytes is None else ws_bytes

@@ -283,6 +283,27 @@ def test_gradient_of_optional_inputs(sdm, gate, skip, bias, state):
     assert (got["ddt_bias"] is None) == (not bias) and got["dstate0"] is None
 
 
+def test_state_gradient_in_place(sdm):
+    """dL/dh0 may be written over dL/dhT."""
+    from sparse_memory_linear_pkm_b200 import native
+
+    v = make(2, 200, 20, 16, seed=6)
+    g = torch.Generator().manual_seed(7)
+    dy, ds = torch.randn(2, 200, 20, generator=g).cuda(), torch.randn(2, 20, 16, generator=g).cuda()
+    want = gradients(sdm, v, dy, ds)
+    out = {k: torch.empty_like(t) for k, t in want.items() if k != "dstate0"}
+    shape = native.SelscanShape(2, 200, 20, 16, 1, native.F32, 1, 0, 0, 0, 0, 0, 0)
+    lib = native.load()
+    n = lib.sdm_selective_scan_backward_workspace_bytes(shape)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    native.check(lib.sdm_selective_scan_backward(
+        shape, *(p(v[k]) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "lengths", "state")), p(dy), p(ds),
+        *(p(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias")), p(ds), p(ws), n,
+        torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(ds, want["dstate0"]) and all(torch.equal(out[k], want[k]) for k in out)
+
+
 def test_gradient_against_differences(sdm):
     v = make(2, 37, 6, 5, 2, seed=4)
     g = torch.Generator().manual_seed(5)
