@@ -527,8 +527,8 @@ SDM_API sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtyp
  *   lengths [B] int32 or NULL: tokens of each row; y of later tokens is left as
  *          it was and their x is not read. Values outside [0, T] are clamped
  *          and set the device error word.
- *   y      [B,T,D] in_dtype; y and state must not overlap x or one another
- *          (refused). */
+ *   y      [B,T,D] in_dtype; y and state must not overlap an input or one
+ *          another (refused). */
 SDM_API sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, const void* w, const void* bias,
                             int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K, int32_t silu, void* state,
                             const int32_t* lengths, void* y, void* stream);
@@ -539,8 +539,8 @@ SDM_API size_t sdm_short_conv_backward_workspace_bytes(int32_t B, int32_t T, int
 /* Gradient of sdm_short_conv for dy = dL/dy and dstate = dL/d(final state)
  * (NULL: none); state0 is the state that the forward started from (NULL: zeros).
  *   dx [B,T,D] in_dtype (0 for tokens past a row's length); dw [D,K] fp32;
- *   dbias [D] fp32 or NULL; dstate0 [B,K-1,D] in_dtype or NULL; dx and dstate0
- *   must not overlap an input (refused). Deterministic. */
+ *   dbias [D] fp32 or NULL; dstate0 [B,K-1,D] in_dtype or NULL; outputs
+ *   must not overlap an input or one another (refused). Deterministic. */
 SDM_API sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in_dtype, const void* w,
                                      const void* bias, int32_t w_dtype, int32_t B, int32_t T, int32_t D, int32_t K,
                                      int32_t silu, const void* state0, const int32_t* lengths, const void* dy,

@@ -116,9 +116,13 @@ sdm_status_t sdm_short_conv(const void* x, int64_t x_stride, int32_t in_dtype, c
   const int64_t tokens = static_cast<int64_t>(B) * T;
   // (Threads read their neighbours' inputs.)
   const size_t row = static_cast<size_t>(D) * es, sb = static_cast<size_t>(B) * (K - 1) * row;
-  const Piece ins[] = {{"x", x, (static_cast<size_t>(tokens - 1) * stride) * es + row}};
+  const size_t ws = in_size(w_dtype) * D;
+  const Piece ins[] = {{"x", x, (static_cast<size_t>(tokens - 1) * stride) * es + row},
+                       {"w", w, ws * K},
+                       {"bias", bias, ws},
+                       {"lengths", lengths, B * sizeof(int32_t)}};
   const Piece outs[] = {{"y", y, static_cast<size_t>(tokens) * row}, {"state", state, sb}};
-  if ((r = check_apart(outs, 2, ins, 1)) != SDM_OK) return r;
+  if ((r = check_apart(outs, 2, ins, 4)) != SDM_OK) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
   const bool vec = whole_units(x, stride, D, in_dtype);
@@ -179,9 +183,15 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   const Piece ins[] = {{"x", x, (static_cast<size_t>(tokens - 1) * stride) * es + row},
                        {"dy", dy, nb},
                        {"state0", state0, sb},
-                       {"dstate", dstate, sb}};
-  const Piece outs[] = {{"dx", dx, nb}, {"dstate0", dstate0, sb}};
-  if ((r = check_apart(outs, 2, ins, 4)) != SDM_OK) return r;
+                       {"dstate", dstate, sb},
+                       {"w", w, in_size(w_dtype) * D * K},
+                       {"bias", bias, in_size(w_dtype) * D},
+                       {"lengths", lengths, B * sizeof(int32_t)}};
+  const Piece outs[] = {{"dx", dx, nb},
+                        {"dstate0", dstate0, sb},
+                        {"dw", dw, sizeof(float) * D * K},
+                        {"dbias", dbias, sizeof(float) * D}};
+  if ((r = check_apart(outs, 4, ins, 7)) != SDM_OK) return r;
   if (p.slots > 65535) return fail(SDM_ERR_UNSUPPORTED, "B * T above 65535 * 512 tokens");
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;

@@ -113,6 +113,28 @@ def test_conv_empty_and_gradient(lib):
     refused(lib, lib.sdm_short_conv_backward(*args), "dstate0 overlaps")
 
 
+def test_conv_refuses_outputs_on_any_input(lib):
+    """Taps, bias and lengths count as inputs too, and the parameters' gradients as outputs."""
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(12)]
+    for name, on in (("y", ("w", "bias", "lengths")), ("state", ("w", "bias", "lengths"))):
+        for i, n in enumerate(on):
+            kw = dict(x=far[0], w=far[1], bias=far[2], lengths=far[3], state=far[4], y=far[5])
+            kw[name] = far[1 + i]
+            refused(lib, lib.sdm_short_conv(*conv_args(**kw)), f"{name} overlaps {n}")
+    need = lib.sdm_short_conv_backward_workspace_bytes(2, 9, 24, 4)
+    names = {0: "x", 3: "w", 4: "bias", 11: "state0", 12: "lengths", 13: "dy", 14: "dstate", 15: "dx", 16: "dw",
+             17: "dbias", 18: "dstate0"}
+    base = [far[0], 0, native.BF16, far[1], far[2], native.F32, 2, 9, 24, 4, 1, *far[3:11], P, need, None]
+    for i in (15, 16, 17, 18):
+        for j in names:
+            if i != j:
+                args = list(base)
+                args[i] = args[j]
+                status = lib.sdm_short_conv_backward(*args)
+                assert status == 1 and b" overlaps " in lib.sdm_last_error(), (names[i], names[j], status)
+                assert names[i].encode() in lib.sdm_last_error() and names[j].encode() in lib.sdm_last_error()
+
+
 def shape(**kw):
     d = dict(B=2, T=40, D=32, N=16, G=1, in_dtype=native.BF16, softplus=1, reserved=0, x_stride=0, dt_stride=0,
              z_stride=0, b_stride=0, c_stride=0)
