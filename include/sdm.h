@@ -481,10 +481,11 @@ SDM_API sdm_status_t sdm_layer_forward_noalloc(const sdm_shape_t* shape, const v
  *     2^-126), code = round-to-nearest-even of y / scale onto the E4M3 grid.
  * Values that are not numbers give the code 0x7F and do not count for a scale.
  *   x [n_rows, d] x_dtype; residual [n_rows, d] res_dtype or NULL; w [d] w_dtype
- *   h [n_rows, d] res_dtype out, with a residual only; may be residual itself
- *   y may be x itself where the types agree. d in [1, 8192]; rows that are a
- *   multiple of 8 values are moved in 16-byte units. scales: as above, NULL
- *   for the other types. The sum of squares is held in 64 bits for the 8-bit
+ *   h [n_rows, d] res_dtype out, with a residual only
+ *   h and y may be x itself or residual itself where the types agree; otherwise
+ *   outputs must not overlap an input or one another (refused). d in [1, 8192];
+ *   rows that are a multiple of 8 values are moved in 16-byte units. scales: as
+ *   above, NULL for the other types. The sum of squares is held in 64 bits for the 8-bit
  *   types and in fp32 for the others and the gradient; a row whose squares leave
  *   fp32's range (tiny ones with eps near 0, huge ones) is first brought into it
  *   by a power of two. */
@@ -509,8 +510,9 @@ SDM_API size_t sdm_rmsnorm_residual_backward_workspace_bytes(int64_t n_rows, int
  *   dw = sum over rows of dy h s
  * For an 8-bit output this is the derivative with the rounding passed over.
  *   h [n_rows, d] h_dtype (x without a residual); w [d]; dy [n_rows, d] dy_dtype;
- *   dh, dx [n_rows, d] h_dtype (dx may be dh, or dy where the types agree);
- *   dw [d] fp32 out. Deterministic. */
+ *   dh, dx [n_rows, d] h_dtype; dw [d] fp32 out. dx may be h itself, dh itself
+ *   or, where the types agree, dy itself; otherwise outputs must not overlap an
+ *   input or one another (refused). Deterministic. */
 SDM_API sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtype, const void* w, int32_t w_dtype,
                                            const void* dy, int32_t dy_dtype, const void* dh, int64_t n_rows,
                                            int32_t d, float eps, void* dx, float* dw, void* workspace,

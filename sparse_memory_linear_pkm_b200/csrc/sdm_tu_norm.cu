@@ -59,6 +59,12 @@ sdm_status_t check_norm(int64_t n_rows, int32_t d, float eps) {
   return SDM_OK;
 }
 
+// An input that an output may take the place of: nothing to check where it does,
+// value for value (a thread reads its values of a row before it writes them).
+Piece unless_same(const Piece& in, int32_t in_dtype, const void* out, int32_t out_dtype) {
+  return in.p == out && in_dtype == out_dtype ? Piece{in.name, nullptr, 0} : in;
+}
+
 template <typename Tx, typename Tr, int kOut, int kW>
 void launch_norm_width(const NormPlan& p, unsigned grid, const sdm::NormArgs& a, cudaStream_t st) {
   if (p.block) sdm::k_rmsnorm_residual<Tx, Tr, kOut, true, kW><<<grid, p.threads, 0, st>>>(a);
@@ -155,6 +161,19 @@ sdm_status_t sdm_rmsnorm_residual(const void* x, int32_t x_dtype, const void* re
   if (any && y_dtype == SDM_FP8_ROW && reinterpret_cast<uintptr_t>(scales) % 4 != 0)
     return fail(SDM_ERR_INVALID_ARGUMENT, "scales is not aligned to its element size");
   if (!any) return ok();
+  const size_t n = static_cast<size_t>(n_rows) * d;
+  const Piece in_x{"x", x, n * in_size(x_dtype)}, in_r{"residual", residual, n * in_size(res_dtype)};
+  const Piece in_w{"w", w, d * in_size(w_dtype)};
+  const Piece out_h{"h", res ? h : nullptr, n * in_size(res_dtype)}, out_y{"y", y, fp8 ? n : n * in_size(y_dtype)};
+  const Piece out_s{"scales", fp8 ? scales : nullptr,
+                    y_dtype == SDM_FP8_ROW ? static_cast<size_t>(n_rows) * sizeof(float) : n / 16};
+  const Piece outs[] = {out_h, out_y, out_s}, fixed[] = {in_w};
+  const Piece for_h[] = {unless_same(in_x, x_dtype, h, res_dtype), unless_same(in_r, res_dtype, h, res_dtype)};
+  const Piece for_y[] = {unless_same(in_x, x_dtype, y, y_dtype), unless_same(in_r, res_dtype, y, y_dtype)};
+  const Piece for_s[] = {in_x, in_r};
+  if ((r = check_apart(&out_h, 1, for_h, 2)) || (r = check_apart(&out_y, 1, for_y, 2)) ||
+      (r = check_apart(&out_s, 1, for_s, 2)) || (r = check_apart(outs, 3, fixed, 1)))
+    return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;
   const NormPlan p = norm_plan(d);
@@ -230,6 +249,16 @@ sdm_status_t sdm_rmsnorm_residual_backward(const void* h, int32_t h_dtype, const
   if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
   if (workspace_bytes < sdm_rmsnorm_residual_backward_workspace_bytes(n_rows, d))
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_rmsnorm_residual_backward_workspace_bytes");
+  const size_t n = static_cast<size_t>(n_rows) * d;
+  const Piece in_h{"h", h, n * in_size(h_dtype)}, in_dy{"dy", dy, n * in_size(dy_dtype)};
+  const Piece in_dh{"dh", dh, n * in_size(h_dtype)}, in_w{"w", w, d * in_size(w_dtype)};
+  const Piece outs[] = {{"dx", dx, n * in_size(h_dtype)}, {"dw", dw, d * sizeof(float)}};
+  const Piece for_dx[] = {unless_same(in_h, h_dtype, dx, h_dtype), unless_same(in_dy, dy_dtype, dx, h_dtype),
+                          unless_same(in_dh, h_dtype, dx, h_dtype), in_w};
+  const Piece for_dw[] = {in_h, in_dy, in_dh, in_w};
+  if ((r = check_apart(outs, 1, for_dx, 4)) || (r = check_apart(outs + 1, 1, for_dw, 4)) ||
+      (r = check_apart(outs, 2, nullptr, 0)))
+    return r;
   const NormPlan p = norm_plan(d);
   const unsigned grid = norm_grid(p, n_rows, 148, kGradThreadsPerSm);
   float* part = static_cast<float*>(workspace);

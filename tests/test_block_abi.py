@@ -61,6 +61,34 @@ def test_norm_empty_and_sizes(lib):
     refused(lib, lib.sdm_rmsnorm_residual_backward(*args), "dy_dtype")
 
 
+def test_norm_refuses_overlaps(lib):
+    """An output may take a whole input's place where the types agree, not part of it or in another type."""
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(8)]
+    next_row = lambda p, size=2: ctypes.c_void_p(p.value + 32 * size)  # noqa: E731
+    base = dict(x=far[0], residual=far[1], res_dtype=native.BF16, w=far[2], h=far[3], y=far[4])
+    for kw, text in ((dict(h=next_row(far[1])), "h overlaps residual"), (dict(h=next_row(far[0])), "h overlaps x"),
+                     (dict(y=next_row(far[0])), "y overlaps x"), (dict(y=next_row(far[1])), "y overlaps residual"),
+                     (dict(y=far[3]), "y overlaps h"), (dict(h=far[2]), "h overlaps w"), (dict(y=far[2]), "y overlaps w"),
+                     (dict(res_dtype=native.F32, h=far[0]), "h overlaps x"),
+                     (dict(y_dtype=native.F32, y=far[0]), "y overlaps x"),
+                     (dict(y_dtype=native.FP8_ROW, y=far[0], scales=far[5]), "y overlaps x"),
+                     (dict(y_dtype=native.FP8_B16, y=far[1], scales=far[5]), "y overlaps residual"),
+                     (dict(y_dtype=native.FP8_ROW, scales=far[4]), "scales overlaps y"),
+                     (dict(y_dtype=native.FP8_B16, scales=far[3]), "scales overlaps h"),
+                     (dict(y_dtype=native.FP8_B16, scales=far[1]), "scales overlaps residual")):
+        refused(lib, lib.sdm_rmsnorm_residual(*norm_args(**(base | kw))), text)
+    size = lib.sdm_rmsnorm_residual_backward_workspace_bytes(3, 2048)
+    base = [far[0], native.BF16, far[1], native.F32, far[2], native.F32, far[3], 3, 2048, 1e-6, far[4], far[5], P, size, None]
+    row = lambda p: ctypes.c_void_p(p.value + 2048 * 2)  # noqa: E731
+    for at, value, text in ((10, row(far[0]), "dx overlaps h"), (10, row(far[3]), "dx overlaps dh"),
+                            (10, far[2], "dx overlaps dy"), (10, far[1], "dx overlaps w"), (11, far[0], "dw overlaps h"),
+                            (11, far[1], "dw overlaps w"), (11, far[2], "dw overlaps dy"), (11, far[3], "dw overlaps dh"),
+                            (11, far[4], "dw overlaps dx")):
+        args = list(base)
+        args[at] = value
+        refused(lib, lib.sdm_rmsnorm_residual_backward(*args), text)
+
+
 def test_decoding_refuses(lib):
     refused(lib, lib.sdm_dequantize_fp8blk(None, P, 1, P, native.F32, None), "codes is NULL")
     refused(lib, lib.sdm_dequantize_fp8blk(P, None, 1, P, native.F32, None), "exps is NULL")

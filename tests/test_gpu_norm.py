@@ -142,6 +142,32 @@ def test_decoding(sdm, dtype):
     assert sdm.dequantize_fp8blk(state, xs.shape).shape == xs.shape
 
 
+@pytest.mark.parametrize("rows,d", [(9, 640), (70, 24), (5, 1001)])
+def test_every_place_an_output_may_take(sdm, rows, d):
+    """h and y over x or the residual, dx over h, dh or dy: the bits of separate outputs."""
+    from sparse_memory_linear_pkm_b200 import native
+
+    lib, st = native.load(), torch.cuda.current_stream().cuda_stream
+    xs, w, r = make(rows, d, BF16, BF16, seed=4)
+    want_y, want_h = sdm.rmsnorm_residual(xs, w, r)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    for h_at, y_at in (("r", "x"), ("x", "r"), ("h", "x"), ("h", "r"), ("r", "y"), ("x", "y")):
+        t = {"x": xs.clone(), "r": r.clone(), "h": torch.empty_like(r), "y": torch.empty_like(xs)}
+        native.check(lib.sdm_rmsnorm_residual(p(t["x"]), native.BF16, p(t["r"]), native.BF16, p(w), native.F32, rows, d,
+                                              1e-6, p(t[h_at]), p(t[y_at]), native.BF16, None, st))
+        assert torch.equal(t[h_at], want_h) and torch.equal(t[y_at], want_y)
+    dy, dh = (torch.randn(rows, d, generator=torch.Generator().manual_seed(i)).to(BF16).cuda() for i in range(2))
+    want = sdm.rmsnorm_residual_backward(want_h, w, dy, dh)
+    n = lib.sdm_rmsnorm_residual_backward_workspace_bytes(rows, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for at in ("h", "dy", "dh"):
+        t = {"h": want_h.clone(), "dy": dy.clone(), "dh": dh.clone()}
+        dw = torch.empty(d, device="cuda")
+        native.check(lib.sdm_rmsnorm_residual_backward(p(t["h"]), native.BF16, p(w), native.F32, p(t["dy"]), native.BF16,
+                                                       p(t["dh"]), rows, d, 1e-6, p(t[at]), p(dw), p(ws), n, st))
+        assert torch.equal(t[at], want[0]) and torch.equal(dw, want[1])
+
+
 def rows_of_scales(d, dtype, seed=0):
     """Rows whose squares leave fp32's range and rows that do not, side by side."""
     scales = [1e-44, 1e-42, 1e-38, 1.0, 1e-30, 1e-25, 3e-21, 1e-19, 1e-18, 1e-16, 3e15, 1e17, 1e20, 2.0, 1e30, 3e37]
