@@ -495,7 +495,7 @@ SDM_API sdm_status_t sdm_rmsnorm_residual(const void* x, int32_t x_dtype, const 
 
 /* fp32 or bf16 values of the 8-bit formats: out = E4M3(code) * 2^exps (per 16
  * values; codes, exps as sdm_quantize_fp8blk writes them), or E4M3(code) *
- * scales[row], rounded once to out_dtype. */
+ * scales[row], rounded once to out_dtype. out must not overlap an input (refused). */
 SDM_API sdm_status_t sdm_dequantize_fp8blk(const uint8_t* codes, const int8_t* exps, int64_t n_blocks, void* out,
                                    int32_t out_dtype, void* stream);
 SDM_API sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, int64_t n_rows, int32_t d,

@@ -201,6 +201,9 @@ sdm_status_t sdm_dequantize_fp8blk(const uint8_t* codes, const int8_t* exps, int
   if ((r = need_ptr(codes, "codes", any)) || (r = need_ptr(out, "out", any))) return r;
   if (any && exps == nullptr) return fail(SDM_ERR_INVALID_ARGUMENT, "exps is NULL");
   if (!any) return ok();
+  const size_t n = static_cast<size_t>(n_blocks) * 16;
+  const Piece ins[] = {{"codes", codes, n}, {"exps", exps, n / 16}}, outs[] = {{"out", out, n * in_size(out_dtype)}};
+  if ((r = check_apart(outs, 1, ins, 2)) != SDM_OK) return r;
   return dequantize<true>(codes, exps, 2 * n_blocks, 2, out, out_dtype, stream);
 }
 
@@ -215,6 +218,10 @@ sdm_status_t sdm_dequantize_fp8row(const uint8_t* codes, const float* scales, in
       (r = need_ptr(out, "out", any)))
     return r;
   if (!any) return ok();
+  const size_t rows = static_cast<size_t>(n_rows), n = rows * d;
+  const Piece ins[] = {{"codes", codes, n}, {"scales", scales, rows * sizeof(float)}};
+  const Piece outs[] = {{"out", out, n * in_size(out_dtype)}};
+  if ((r = check_apart(outs, 1, ins, 2)) != SDM_OK) return r;
   return dequantize<false>(codes, scales, n_rows * (d / 8), d / 8, out, out_dtype, stream);
 }
 

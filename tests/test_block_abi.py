@@ -100,6 +100,17 @@ def test_decoding_refuses(lib):
     assert lib.sdm_dequantize_fp8row(None, None, 0, 32, None, native.F32, None) == 0
 
 
+def test_decoding_refuses_overlaps(lib):
+    """A value takes more room than its code: decoding in place would write codes that are still to be read."""
+    a, b, o = (ctypes.c_void_p(i << 24) for i in (2, 3, 4))
+    for out, text in ((a, "out overlaps codes"), (ctypes.c_void_p(a.value + 496), "out overlaps codes")):
+        refused(lib, lib.sdm_dequantize_fp8blk(a, b, 32, out, native.BF16, None), text)
+        refused(lib, lib.sdm_dequantize_fp8row(a, b, 16, 32, out, native.F32, None), text)
+    refused(lib, lib.sdm_dequantize_fp8blk(a, b, 32, b, native.F32, None), "out overlaps exps")
+    refused(lib, lib.sdm_dequantize_fp8row(a, b, 16, 32, b, native.BF16, None), "out overlaps scales")
+    refused(lib, lib.sdm_dequantize_fp8blk(a, ctypes.c_void_p(o.value + 64), 32, o, native.F32, None), "out overlaps exps")
+
+
 def conv_args(**kw):
     d = dict(x=P, x_stride=0, in_dtype=native.BF16, w=P, bias=P, w_dtype=native.F32, B=2, T=9, D=24, K=4, silu=1,
              state=P, lengths=P, y=ctypes.c_void_p(1 << 24), stream=None)
