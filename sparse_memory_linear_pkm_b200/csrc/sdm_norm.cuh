@@ -415,16 +415,31 @@ __global__ void __launch_bounds__(kBlock ? kNormMaxThreads : 128, kBlock ? 2 : 8
 
 // ----------------------------------------------------------------- decoding --
 
-// Eight codes (value i in byte i) times a scale.
+// Eight codes (value i in byte i) times a scale, as fp32 values that round to Ty as
+// the products themselves do. The product of a 4-bit and a 24-bit value has 28
+// bits; rounded to fp32 first, one in 2^17 lands on a border of bf16 that it is not
+// on. (kExact: the scale is a power of two, and no bits are lost.)
+template <typename Ty, bool kExact>
 __device__ __forceinline__ void e4m3_values8(uint2 u, float scale, float* out) {
   const uint32_t w[2] = {u.x, u.y};
+  float c[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-    out[2 * i] = f.x * scale;
-    out[2 * i + 1] = f.y * scale;
+    c[2 * i] = f.x;
+    c[2 * i + 1] = f.y;
+  }
+  bool border = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    out[i] = c[i] * scale;
+    if (!kExact && sizeof(Ty) == 2) border |= (__float_as_uint(out[i]) & 0xFFFFu) == 0x8000u;
+  }
+  if (border) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = to_f32_odd(static_cast<double>(c[i]) * static_cast<double>(scale));
   }
 }
 
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(256) k_dequantize_fp8(const uint8_t* __restric
     const float scale = kBlocks ? pow2f(static_cast<const int8_t*>(scales)[u / 2])
                                 : static_cast<const float*>(scales)[u / units_per_row];
     float v[8];
-    e4m3_values8(reinterpret_cast<const uint2*>(codes)[u], scale, v);
+    e4m3_values8<Ty, kBlocks>(reinterpret_cast<const uint2*>(codes)[u], scale, v);
     store8<Ty>(out + 8 * u, v);
   }
 }

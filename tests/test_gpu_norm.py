@@ -209,6 +209,37 @@ def test_infinite_values_of_a_row(sdm):
             assert torch.equal(y[r], clean[r])
 
 
+def bf16_of(v: torch.Tensor) -> torch.Tensor:
+    """64-bit values rounded to bf16 once: through fp32 cut off with its last bit set where something was."""
+    f = v.float()
+    odd = (f.view(torch.int32) - (f.double().abs() > v.abs()).int()) | (f.double() != v).int()
+    return torch.where(torch.isfinite(f), odd.view(torch.float32), f).to(BF16)
+
+
+def test_decoding_rounds_once(sdm):
+    """Products of all codes with scales all over the range, also those whose fp32 rounding lies on a border of bf16,
+    equal the real product rounded once; a scale that is not finite gives what its product is."""
+    g = torch.Generator().manual_seed(0)
+    scales = torch.exp2(torch.rand(8192, generator=g) * 270 - 149)
+    scales[:4] = torch.tensor([float("inf"), float("nan"), 0.0, 2.0 ** -149])
+    # 24-bit significands whose product with m = 9, 11, 13 or 15 is next to a border, an odd multiple of half a step
+    near = torch.cat([(torch.arange(257, 512, 2) * 2.0 ** k / m).round() for m in (9, 11, 13, 15) for k in (18, 19, 20)])
+    near = near[(near >= 2 ** 23) & (near < 2 ** 24)].float()
+    scales[4:4 + near.numel()] = near * torch.exp2(torch.arange(near.numel()) % 200 - 140.0)
+    codes = torch.arange(256, dtype=torch.uint8).repeat(8192, 1)
+    grid = torch.cat([ref.e4m3_grid(), torch.full((1,), float("nan")).double()])
+    values = torch.cat([grid, -grid])
+    exact = values[codes.long()] * scales.double()[:, None]
+    want = bf16_of(exact)
+    nan = torch.isnan(exact)
+    assert int((exact.float().to(BF16) != want)[~nan].sum()) > 100  # where rounding twice differs
+    got = sdm.dequantize_fp8row(codes.cuda().view(torch.float8_e4m3fn), scales.cuda(), BF16).cpu()
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan])
+    wide = sdm.dequantize_fp8row(codes.cuda().view(torch.float8_e4m3fn), scales.cuda()).cpu()
+    assert torch.equal(wide[~nan], exact.float()[~nan])
+
+
 def test_in_place_residual_and_output(sdm):
     xs, w, r = make(9, 640, BF16, BF16, seed=4)
     y, h = sdm.rmsnorm_residual(xs, w, r)
