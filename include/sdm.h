@@ -627,7 +627,8 @@ SDM_API size_t sdm_grad_norm_clip_workspace_bytes(int32_t n_tensors);
  * max_norm may be infinite (c = 1 whatever the norm is: out_i = grad_i). Squares
  * beyond fp32's range are summed in 64 bits; a norm that is not finite gives c =
  * 0 or not a number for a finite max_norm, as the formula does. An output that shares memory with another tensor of the list
- * (the same tensor twice, in place) or with part of its own gradient is refused.
+ * (the same tensor twice, in place) or with part of its own gradient is refused,
+ * and so is a norm inside a tensor.
  * The sums have a fixed order. */
 SDM_API sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tensors, float max_norm, float eps,
                                 float* norm, void* workspace, size_t workspace_bytes, void* stream);

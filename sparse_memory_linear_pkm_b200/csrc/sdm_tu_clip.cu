@@ -173,6 +173,14 @@ sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tens
   if ((r = need_ptr(workspace, "workspace", true)) != SDM_OK) return r;
   if (workspace_bytes < sdm_grad_norm_clip_workspace_bytes(n_tensors))
     return fail(SDM_ERR_INVALID_ARGUMENT, "workspace is smaller than sdm_grad_norm_clip_workspace_bytes");
+  // The second pass writes the norm while it reads gradients and writes outputs.
+  const Piece own{"norm", norm, sizeof(float)};
+  for (int i = 0; i < n_tensors; ++i) {
+    const sdm_grad_tensor_t& t = tensors[i];
+    const size_t n = static_cast<size_t>(t.n);
+    if (overlap(own, {"grad", t.grad, n * in_size(t.dtype)}) || overlap(own, {"out", t.out, n * in_size(t.out_dtype)}))
+      return fail(SDM_ERR_INVALID_ARGUMENT, "norm overlaps tensors[" + std::to_string(i) + "]");
+  }
   double* slots = static_cast<double*>(workspace);
   sdm::ClipTable table;
   int n_slots = 0;

@@ -305,6 +305,18 @@ def test_clip_refuses(lib):
     assert lib.sdm_grad_norm_clip_workspace_bytes(-1) == 0
 
 
+def test_clip_refuses_a_norm_inside_a_tensor(lib):
+    """The pass that writes the norm reads gradients and writes outputs at the same time."""
+    a, o, far = 1 << 24, 1 << 25, 1 << 26
+    good = (far, far + (1 << 20), 100, native.F32, native.F32)
+    for entry in ((a, o, 100, native.F32, native.F32), (a, o, 100, native.BF16, native.F32),
+                  (a, o, 200, native.F32, native.BF16), (a, a, 100, native.F32, native.F32)):
+        for at, size in ((entry[0], 2 if entry[3] else 4), (entry[1], 2 if entry[4] else 4)):
+            for norm in (at, at + entry[2] * size - 4):
+                refused(lib, clip(lib, [good, entry], norm=ctypes.c_void_p(norm)), "norm overlaps tensors[1]")
+    refused(lib, clip(lib, [good, (a, None, 10, 0, 0)], norm=ctypes.c_void_p(a)), "norm overlaps tensors[1]")
+
+
 def test_front_end_has_no_cpu_path():
     import sparse_memory_linear_pkm_b200 as sdm
 

@@ -109,6 +109,27 @@ def test_infinite_max_norm_copies_whatever_the_norm_is(sdm, value, dtype, out_dt
     assert torch.equal(torch.nan_to_num(g, nan=7.0), torch.nan_to_num(before, nan=7.0))
 
 
+def test_norm_beside_its_tensors(sdm):
+    """The norm's place may touch a tensor, or be where one without values points."""
+    from sparse_memory_linear_pkm_b200 import native
+
+    lib = native.load()
+    flat = torch.randn(2001, generator=torch.Generator().manual_seed(6)).cuda()
+    want = flat.clone()
+    n = total([want[:1000], want[1001:]])
+    at = flat.data_ptr()
+    table = (native.GradTensor * 3)(native.GradTensor(at, at, 1000, native.F32, native.F32),
+                                    native.GradTensor(at + 4000, None, 0, native.F32, native.F32),
+                                    native.GradTensor(at + 4004, at + 4004, 1000, native.F32, native.F32))
+    ws = torch.empty(lib.sdm_grad_norm_clip_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+    native.check(lib.sdm_grad_norm_clip(table, 3, 1.0, 1e-6, at + 4000, ws.data_ptr(), ws.numel(),
+                                        torch.cuda.current_stream().cuda_stream))
+    assert abs(float(flat[1000]) - n) <= 6 * ref.U * n
+    want[1000] = 0
+    flat[1000] = 0
+    ref.assert_within(flat, ref.d(want) / (n + 1e-6), 8 * ref.U * ref.d(want).abs(), "scaled")
+
+
 def test_same_bits_every_time(sdm):
     g = [torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda() for n in (1_000_003, 77, 250_000)]
     first = sdm.grad_norm_clip(g, float("inf"))
