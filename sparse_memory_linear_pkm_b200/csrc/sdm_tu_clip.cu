@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
 #include <vector>
 
 #include "sdm_check.h"
@@ -47,7 +48,7 @@ sdm_status_t check_tensor(const sdm_grad_tensor_t& t, int i) {
 // list names first: the second pass reads and writes in any order. A sweep over
 // all pieces by address, with the two furthest ends of pieces so far that belong
 // to different tensors (one is always another's), of all pieces and of outputs.
-sdm_status_t check_outputs_apart(const sdm_grad_tensor_t* t, int n) {
+sdm_status_t check_outputs_apart(const sdm_grad_tensor_t* t, int n) try {
   struct Span {
     uintptr_t begin, end;
     int of;
@@ -98,6 +99,8 @@ sdm_status_t check_outputs_apart(const sdm_grad_tensor_t* t, int n) {
     if (s.out) outs.add(s.end, s.of);
   }
   return SDM_OK;
+} catch (const std::bad_alloc&) {  // nothing is thrown past a C entry point
+  return fail(SDM_ERR_UNSUPPORTED, "not enough host memory to check the list");
 }
 
 // Chunks small enough that few values still spread over all blocks, and large

@@ -2,6 +2,9 @@
 and their sizes, without a GPU."""
 
 import ctypes
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -315,6 +318,30 @@ def test_clip_refuses_a_norm_inside_a_tensor(lib):
             for norm in (at, at + entry[2] * size - 4):
                 refused(lib, clip(lib, [good, entry], norm=ctypes.c_void_p(norm)), "norm overlaps tensors[1]")
     refused(lib, clip(lib, [good, (a, None, 10, 0, 0)], norm=ctypes.c_void_p(a)), "norm overlaps tensors[1]")
+
+
+LITTLE_MEMORY = """
+import ctypes, resource
+import torch
+from sparse_memory_linear_pkm_b200 import native
+lib = native.load()
+n = 2_000_000
+rows = torch.zeros(n, 4, dtype=torch.int64)
+rows[:, 0] = rows[:, 1] = (1 << 30) + 64 * torch.arange(n)
+rows[:, 2] = 8
+pages = int(open("/proc/self/statm").read().split()[0])
+resource.setrlimit(resource.RLIMIT_AS, (pages * resource.getpagesize() + (16 << 20),) * 2)
+status = lib.sdm_grad_norm_clip(rows.data_ptr(), n, 1.0, 1e-6, 1 << 20, 1 << 20, 1 << 40, None)
+print(status, lib.sdm_last_error().decode())
+"""
+
+
+def test_clip_reports_a_lack_of_host_memory(lib):
+    """No C++ exception leaves the library: a list whose check finds no memory returns an error."""
+    got = subprocess.run([sys.executable, "-c", LITTLE_MEMORY], cwd=Path(__file__).resolve().parent.parent,
+                         capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0, got.stderr[-500:]
+    assert got.stdout.startswith("2 not enough host memory"), got.stdout
 
 
 def test_front_end_has_no_cpu_path():
