@@ -128,3 +128,42 @@ def scan_step_error(dt, A, dt_bias, softplus=True):
     rel = 2.0 ** -21 + 2.0 ** -22 * float(u.abs().max() if u.numel() else 0.0)
     T = dt.shape[1]
     return 2.0 ** -21 + 4 * U + rel * (1 + span) + span * (T + 8) * U
+
+
+def scan_errors(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, lengths=None):
+    """Bounds of the errors of an fp32 selective scan (y before its own rounding, final state), elementwise, with every
+    step's error weighted by the decay that still applies to it: err_t = a_t err_{t-1} + what the step adds.
+
+    That is, relative to the terms' absolute values: the step size's error (its exponential and polynomial 2^-21, its
+    argument 2^-22 |u|) and 4 roundings for the input; for the state's decay its exponential (2^-22, and 4 roundings)
+    and |delta_t A| times the step size's error and T + 8 roundings, which covers a split's summed step sizes: each of
+    the sum's T roundings is at most 2^-24 of it, and the sum's terms are the tokens' step sizes."""
+    T, N = x.shape[1], A.shape[1]
+    rep = x.shape[2] // Bm.shape[2]
+    u = dt if dt_bias is None else dt + dt_bias
+    delta = torch.where(u > 30, u, torch.log1p(torch.exp(u.clamp(max=30))))
+    rel = 2.0 ** -21 + 2.0 ** -22 * u.abs()
+    h = torch.zeros(x.shape[0], x.shape[2], N, dtype=torch.float64, device=x.device) if h0 is None else h0.abs()
+    err = torch.zeros_like(h)
+    out = []
+    for t in range(T):
+        dd = delta[:, t, :, None]
+        a = torch.exp(dd * A)
+        term, r = (dd * x[:, t, :, None] * Bm[:, t].repeat_interleave(rep, 1)).abs(), rel[:, t, :, None]
+        new = a * h + term
+        e = a * err + (2.0 ** -22 + 4 * U + (dd * A).abs() * (r + (T + 8) * U)) * a * h + (r + 4 * U) * term
+        if lengths is not None:
+            on = (t < lengths)[:, None, None]
+            new, e = torch.where(on, new, h), torch.where(on, e, err)
+        h, err = new, e
+        C = Cm[:, t].repeat_interleave(rep, 1).abs()
+        size, b = (C * h).sum(-1), (C * err).sum(-1)
+        if D is not None:
+            size = size + (D * x[:, t]).abs()
+        b = b + (N + 4) * U * size
+        if z is not None:  # the gate's exponential and division, and its product
+            zt = z[:, t]
+            g = (zt * torch.sigmoid(zt)).abs()
+            b = b * g + (6 + 1.2 * zt.abs()) * 2 * U * size * g
+        out.append(b)
+    return torch.stack(out, 1), err
