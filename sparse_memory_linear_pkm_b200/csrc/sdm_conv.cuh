@@ -238,17 +238,24 @@ struct ConvGradArgs {
 
 constexpr int kConvGradLanes = 32, kConvGradRows = 8;   // units x segments of a block
 
+// Blocks an SM holds: three (80 registers) while the taps' windows leave few
+// enough values to spill. Three against two blocks for B = 8, T = 4096, D = 2048:
+// bf16 97 / 115 us with K = 2, 103 / 122 with 3, 112 / 130 with 4 (36 bytes
+// spilled; D = 2047, without whole units, 191 / 187), 272 / 179 with 8; fp32 137 /
+// 156 with 2, 145 / 159 with 3, 164 / 165 with 4 (116 bytes spilled; D = 2047 237 /
+// 178), 274 / 200 with 8.
+constexpr int conv_grad_blocks(int K, size_t value) { return K <= (value == 2 ? 4 : 3) ? 3 : 2; }
+
 // With du = dy act'(u): dx_t = sum_k w[k] du_{t+K-1-k}, dw[k] = sum_t du_t
 // x_{t-K+1+k}, db = sum_t du_t. A thread walks one segment of tokens with the
 // last inputs and du in registers; the block's segments of a channel are added
 // in shared memory in a fixed order, and the blocks' sums by k_short_conv_sums.
 // The extended sequence has K - 1 rows before token 0 (dstate0), and the
-// derivative of the final state reaches the last K - 1 inputs. 111 us for the
+// derivative of the final state reaches the last K - 1 inputs. 112 us for the
 // 0.40 GB of B = 8, T = 4096, D = 2048 in bf16 (3.6 TB/s): 33 instructions a
-// value keep the issue slots 58 % busy at 24 warps an SM. (128 registers and 16
-// warps: 132 us.)
+// value keep the issue slots 58 % busy at 24 warps an SM. fp32: 165 us, 4.9 TB/s.
 template <typename T, int K, bool kVec>
-__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, K <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kConvGradLanes * kConvGradRows, conv_grad_blocks(K, sizeof(T)))
     k_short_conv_backward(const ConvGradArgs a) {
   constexpr int V = kConvV, kAhead = kConvAhead;
   __shared__ float2 sums[kConvGradRows][K + 1][kConvGradLanes];
