@@ -588,7 +588,11 @@ SDM_API sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const 
                                 const float* dt_bias, const int32_t* lengths, const float* h0, float* hT, void* y,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace sdm_selective_scan_backward needs (0 for invalid shapes). */
+/* Bytes of workspace sdm_selective_scan_backward needs (0 for invalid shapes).
+ * Most of it is one state per four tokens: B T D n bytes, n = N rounded up to 8,
+ * 16, 32 or 64 (B = 8, T = 4096, D = 4096: 2 GiB with N = 16, 8 times x in bf16,
+ * and 8 GiB with N = 64), and B T D bytes of sums; then 8 bytes per (token, group, state) and
+ * channel tile (128 channels, 64 for N above 16, 32 for N above 32). */
 SDM_API size_t sdm_selective_scan_backward_workspace_bytes(const sdm_selscan_shape_t* shape);
 
 /* Gradient of sdm_selective_scan for dy = dL/dy and dhT = dL/dhT (NULL: none).
@@ -626,10 +630,10 @@ SDM_API size_t sdm_grad_norm_clip_workspace_bytes(int32_t n_tensors);
  * tensors is a HOST array, read during the call. norm: one fp32 on the device.
  * max_norm may be infinite (c = 1 whatever the norm is: out_i = grad_i). Squares
  * beyond fp32's range are summed in 64 bits; a norm that is not finite gives c =
- * 0 or not a number for a finite max_norm, as the formula does. An output that shares memory with another tensor of the list
- * (the same tensor twice, in place) or with part of its own gradient is refused,
- * and so is a norm inside a tensor.
- * The sums have a fixed order. */
+ * 0 or not a number for a finite max_norm, as the formula does. An output that
+ * shares memory with another tensor of the list (the same tensor twice, in
+ * place) or with part of its own gradient is refused, and so is a norm inside a
+ * tensor. The sums have a fixed order. */
 SDM_API sdm_status_t sdm_grad_norm_clip(const sdm_grad_tensor_t* tensors, int32_t n_tensors, float max_norm, float eps,
                                 float* norm, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -277,10 +277,10 @@ static __global__ void __launch_bounds__(128) k_selective_scan_grad_chain(const 
 
 // Sums of a lane's KS values over the warp's channels (lane bits from log2 L
 // up). Register groups of four values are held in another order in each lane,
-// group j being group j ^ sum_order(lane): what a lane sends in the first
+// group j being group j ^ order(lane): what a lane sends in the first
 // exchanges is then always its upper half, with nothing to select. Returns in
-// v[0 .. kLeft) the sums of values kLeft * sum_place(lane) .. of group
-// sum_order(lane); lanes that differ in the remaining bits hold the same.
+// v[0 .. kLeft) the sums of values kLeft * place(lane) .. of group
+// order(lane); lanes that differ in the remaining bits hold the same.
 template <int KS, int L>
 struct ChannelSum {
   static constexpr int kOrderBits = KS == 16 ? 2 : 1;          // lane bits 4 (and 3)
