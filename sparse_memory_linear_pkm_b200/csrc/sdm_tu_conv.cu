@@ -163,6 +163,8 @@ sdm_status_t sdm_short_conv_backward(const void* x, int64_t x_stride, int32_t in
   if (!any) {
     // No token: the parameters get nothing, and the initial state is the final one.
     const size_t sb = static_cast<size_t>(B) * (K - 1) * D * es;
+    const Piece first = {"dstate0", dstate0, sb}, last = {"dstate", dstate0 == dstate ? nullptr : dstate, sb};
+    if ((r = check_apart(&first, 1, &last, 1)) != SDM_OK) return r;
     cudaError_t e = cudaSuccess;
     if (D > 0) e = cudaMemsetAsync(dw, 0, static_cast<size_t>(D) * K * sizeof(float), st);
     if (e == cudaSuccess && D > 0 && dbias != nullptr) e = cudaMemsetAsync(dbias, 0, D * sizeof(float), st);

@@ -193,11 +193,13 @@ sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x,
       (r = need_ptr(h0, "h0", state && h0 != nullptr)) || (r = need_ptr(hT, "hT", state && hT != nullptr)))
     return r;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t states = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
+  const Piece last = {"hT", hT, states}, start = {"h0", hT == h0 ? nullptr : h0, states};
   if (!any) {
+    if ((r = check_apart(&last, 1, &start, 1)) != SDM_OK) return r;
     if (state && hT != nullptr && hT != h0) {
-      const size_t n = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
-      const cudaError_t e = h0 != nullptr ? cudaMemcpyAsync(hT, h0, n, cudaMemcpyDeviceToDevice, st)
-                                          : cudaMemsetAsync(hT, 0, n, st);
+      const cudaError_t e = h0 != nullptr ? cudaMemcpyAsync(hT, h0, states, cudaMemcpyDeviceToDevice, st)
+                                          : cudaMemsetAsync(hT, 0, states, st);
       if (e != cudaSuccess) return fail(SDM_ERR_CUDA, std::string("state copy: ") + cudaGetErrorString(e));
     }
     return ok();
@@ -210,9 +212,7 @@ sdm_status_t sdm_selective_scan(const sdm_selscan_shape_t* shape, const void* x,
   }
   sdm::SelScanArgs a = selscan_args(s, x, dt, A, Bm, Cm, Dskip, z, dt_bias, lengths);
   const SelInputs in = selscan_inputs(s, a);
-  const size_t states = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
-  const Piece outs[] = {{"y", y, static_cast<size_t>(s.B) * s.T * s.D * in_size(s.in_dtype)}, {"hT", hT, states}};
-  const Piece start = {"h0", hT == h0 ? nullptr : h0, states};
+  const Piece outs[] = {{"y", y, static_cast<size_t>(s.B) * s.T * s.D * in_size(s.in_dtype)}, last};
   if ((r = check_apart(outs, 2, in.piece, kSelInputs)) || (r = check_apart(outs, 2, &start, 1))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;

@@ -116,7 +116,10 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
     return r;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t states = static_cast<size_t>(s.B) * s.D * s.N * sizeof(float);
+  // dh0 may be dhT: one thread reads a value of dhT and writes that of dh0.
+  const Piece first = {"dh0", dh0, states}, last = {"dhT", dhT == dh0 ? nullptr : dhT, states};
   if (!any) {
+    if ((r = check_apart(&first, 1, &last, 1)) != SDM_OK) return r;
     // No token: the parameters get nothing, and dL/dh_0 is dL/dh_T.
     if ((r = cleared(dA, static_cast<size_t>(s.D) * s.N * sizeof(float), st)) ||
         (r = cleared(dD, s.D * sizeof(float), st)) || (r = cleared(ddt_bias, s.D * sizeof(float), st)) ||
@@ -137,10 +140,9 @@ sdm_status_t sdm_selective_scan_backward(const sdm_selscan_shape_t* shape, const
   const size_t es = in_size(s.in_dtype), tokens = static_cast<size_t>(s.B) * s.T, rows = tokens * s.D * es;
   const size_t bc = tokens * s.G * s.N * es;
   const size_t row = s.D * sizeof(float);
-  // (dh0 may be dhT: one thread reads a value of dhT and writes that of dh0.)
-  const Piece more[] = {{"dy", dy, rows}, {"h0", h0, states}, {"dhT", dhT == dh0 ? nullptr : dhT, states}};
+  const Piece more[] = {{"dy", dy, rows}, {"h0", h0, states}, last};
   const Piece outs[] = {{"dx", dx, rows}, {"ddt", ddt, rows}, {"dz", dz, rows},  {"dB", dB, bc},  {"dC", dC, bc},
-                        {"dA", dA, row * s.N}, {"dD", dD, row}, {"ddt_bias", ddt_bias, row}, {"dh0", dh0, states}};
+                        {"dA", dA, row * s.N}, {"dD", dD, row}, {"ddt_bias", ddt_bias, row}, first};
   if ((r = check_apart(outs, 9, in.piece, kSelInputs)) || (r = check_apart(outs, 9, more, 3))) return r;
   DeviceInfo* dev;
   if ((r = device_info(&dev)) != SDM_OK) return r;

@@ -277,6 +277,22 @@ def test_scan_refuses_outputs_on_any_input(lib):
                 assert status == 1 and b" overlaps " in lib.sdm_last_error()
 
 
+def test_calls_without_tokens_refuse_overlapping_states(lib):
+    """There the state is copied: onto itself it stays, onto a part of itself the copy has no order."""
+    a = ctypes.c_void_p(1 << 24)
+    part = ctypes.c_void_p(a.value + 64)
+    s = ctypes.byref(shape(T=0))
+    none = [None] * 9
+    refused(lib, lib.sdm_selective_scan(s, *none, a, part, None, None, 0, None), "hT overlaps h0")
+    assert lib.sdm_selective_scan(s, *none, a, a, None, None, 0, None) == 0
+    far = [ctypes.c_void_p((i + 2) << 24) for i in range(4)]
+    args = [*none, None, None, a, None, None, far[1], None, None, None, None, None, part, None, 0, None]
+    refused(lib, lib.sdm_selective_scan_backward(s, *args), "dh0 overlaps dhT")
+    args = [None, 0, native.BF16, None, None, native.F32, 2, 0, 24, 4, 1, None, None, None, a, None, far[1], None, part,
+            None, 0, None]
+    refused(lib, lib.sdm_short_conv_backward(*args), "dstate0 overlaps dstate")
+
+
 def clip(lib, entries, max_norm=1.0, eps=1e-6, norm=P, ws=P, ws_bytes=None):
     table = (native.GradTensor * max(1, len(entries)))(*[native.GradTensor(*e) for e in entries])
     n = lib.sdm_grad_norm_clip_workspace_bytes(len(entries)) if ws_bytes is None else ws_bytes
