@@ -12,10 +12,10 @@
 // maximum to the exponent's border) is recomputed in 64 bits and rounded to odd
 // before the conversion. Such blocks are about one in two thousand.
 //
-// Bound by memory: 16,384 rows of 2048 (bf16, bf16 residual and output) take 52
-// us, 5.1 TB/s; 16,384 rows of 4096 with an fp32 residual into codes with a scale
-// per row, and their decoding, 183 us for 0.94 GB, 5.1 TB/s; the gradient of
-// 32,768 rows of 2048 88 us, 6.1 TB/s.
+// Bound by memory: 16,384 rows of 2048 (bf16, bf16 residual and output) take 47
+// us, 5.7 TB/s; 16,384 rows of 4096 with an fp32 residual into codes with a scale
+// per row, and their decoding, 181 us for 0.94 GB, 5.2 TB/s (40 bytes a thread
+// spilled at 64 registers); the gradient of 32,768 rows of 2048 88 us, 6.1 TB/s.
 #pragma once
 
 #include <type_traits>

@@ -84,7 +84,9 @@ __device__ __forceinline__ float2 decay2(float2 delta, float2 A2) {
 // softplus of two values: max(u, 0) + log(1 + e), e = exp(-|u|) in (0, 1], with
 // log(1 + e) = e q(e). q is the polynomial of degree 8 with the least relative
 // error on [0, 1] (3e-8, fitted by reweighted least squares at Chebyshev
-// points), so that small results keep their relative accuracy.
+// points), so that small results keep their relative accuracy. The argument of
+// ex2 is rounded once, so that the error grows with |u|: 0.5e-7 relative (root
+// mean square) above -2.3, 1.4e-7 down to -7, 2.4e-7 to -12, 6e-7 to -30.
 __device__ __forceinline__ float2 softplus2(float2 u) {
   const float2 e = make_float2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
   float2 q = both(0.0052326880395412445f);
