@@ -408,7 +408,10 @@ static __global__ void __launch_bounds__(256) k_selective_scan_join(const float*
 // of a thread's loads go out before the first is used. 18.4 us for the 71 MB of B
 // = 128, D = 4096, N = 16, 3.9 TB/s. (Sixteen states a lane: 20.6 us, a sector's
 // halves and too few warps; four: 25.3, the step size and the gate are made four
-// times. N = 32: 27 us instead of 35 with sixteen; N = 12: 14.8 instead of 12.9.)
+// times. N = 32: 27 us instead of 35 with sixteen. N = 9 to 12 fill two lanes badly,
+// but one lane of sixteen is no better rule; from L2, B x 4096, eight / sixteen: N = 12
+// 4.3 / 4.7 us for B = 16, 15.9 / 13.9 for 128, 122 / 117 for 1024; N = 10 18.5 / 23.8
+// for 128.)
 constexpr int kStepThreads = 128;
 
 template <typename T, int KS, int L>
